@@ -491,6 +491,147 @@ HQMQ_API int hqmq_attention_decode(const uint16_t *d_q, const int32_t *d_seq_len
                                    int out_dtype, void *d_ws, uint64_t ws_bytes,
                                    hqmq_status *d_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged cache: a coded K or V cache that grows in place.  The pages' decoder
+ * reads a stored cache (gist.science/nl, Technische Samenvatting, "Memory en
+ * Latentie"); how that cache is laid out while it grows is not given there,
+ * so the layout is this library's.
+ *
+ * A pool of n_pages pages; a page holds page_size tokens of `heads` KV heads
+ * of 128 elements (32 chunks).  A sequence is a row of a block table, int32
+ * [n_seqs][max_pages]: its token at position t lies in page
+ * block_table[b][t / page_size], row t % page_size.  Page ids may come in any
+ * order and several sequences may share a page that none of them writes.
+ * Per token of a head:
+ *   - b index words (32 b-bit indices, LSB first, exactly a packing group);
+ *   - 32 fp16 radii;
+ *   - one flag word, the pages' 1-bit flag (gist.science/nl, Technische
+ *     Samenvatting, section 3): bit c set = chunk c is kept in fp16, its
+ *     index and radius are 0.
+ * The flagged chunks' values of a (page, head) lie in out_val in token and
+ * chunk order from slot 0: those of row t start at slot
+ * sum_{u < t} popcount(flags[u]).  Writing row t therefore needs rows < t of
+ * that page written, and makes rows > t of that page meaningless until they
+ * are written again.  HOST struct of DEVICE pointers, each 16-byte aligned
+ * (thr 4-byte). */
+typedef struct {
+    uint32_t *idx_words;          /* [n_pages][heads][page_size][b]          */
+    uint16_t *radius;             /* [n_pages][heads][page_size][32]         */
+    uint32_t *flags;              /* [n_pages][heads][page_size]; NULL: no outliers */
+    uint16_t *out_val;            /* [n_pages][heads][out_cap][4]            */
+    const float *codebook;        /* fp32 [heads][S][4]                      */
+    const float *thr;             /* fp32 [heads]: outlier threshold, for writing with flags */
+    const void *table;            /* search tables of the heads' codebooks, or NULL; for writing */
+    uint32_t S;                   /* 1 .. 48                                 */
+    int n_pages;
+    int page_size;                /* 16, 32, 64, 128 or 256                  */
+    int heads;                    /* 1 .. 1024                               */
+    int out_cap;                  /* slots of a (page, head), 1 .. 32 page_size; ignored without flags */
+} hqmq_kv_pages;
+
+/* A page id outside [0, n_pages), a position below 0 or a position past the
+ * block table's last page: the tokens concerned are left out. */
+#define HQMQ_FLAG_BAD_PAGE 32u
+
+/* One strided tensor [B][T][heads][D] whose last dimension is contiguous;
+ * strides in elements. */
+typedef struct {
+    void *data;
+    int64_t stride_b, stride_t, stride_h;
+    int heads;
+} hqmq_head_view;
+
+/* RMS norm of every query and key head vector and the position rotation, in
+ * one pass; what the codec and the attention calls are fed with.  Per vector
+ * x of D elements:
+ *   y = x / sqrt(mean(x^2) + eps) * w   (w NULL: y = x);
+ *   the first R elements are rotated in pairs by a_i = pos inv_freq[i]:
+ *     y'_u = y_u cos a_i - y_v sin a_i,  y'_v = y_v cos a_i + y_u sin a_i,
+ *   with (u, v) = (i, i + R/2), or (2 i, 2 i + 1) if interleaved; the rest
+ *   passes through.
+ * Norm, rotation and products in fp32, one rounding to dtype at the end;
+ * a_i in fp64, reduced there, so far positions keep their accuracy.
+ * q or k may be NULL (with its output); q_out / k_out have the same shapes
+ * with strides of their own (k_out in [B][H][T][D] order feeds the encode
+ * calls) and may be the very same view (in place) but not overlap otherwise.
+ * d_q_weight, d_k_weight: [D] of w_dtype or NULL.  d_pos: int32 [B][T].
+ * d_inv_freq: fp64 [R / 2] (NULL if R = 0).  D in [1, 512]; R even, in
+ * [0, D]; eps finite and >= 0; B T may be 0 (nothing is done). */
+HQMQ_API int hqmq_qk_norm_rope(const hqmq_head_view *q, const hqmq_head_view *q_out,
+                               const hqmq_head_view *k, const hqmq_head_view *k_out, int dtype,
+                               int B, int T, int D, const void *d_q_weight,
+                               const void *d_k_weight, int w_dtype, float eps,
+                               const int32_t *d_pos, const double *d_inv_freq, int R,
+                               int interleaved, void *stream);
+
+/* Quantises new tokens straight into the pages, K and V in one launch.
+ * Sequence b's new tokens are rows d_cu_tokens[b] .. d_cu_tokens[b+1] - 1 of
+ * d_xk and d_xv ([n_tokens][heads][128] of dtype, strides in elements, the
+ * last dimension contiguous) and take the positions d_pos0[b], d_pos0[b] + 1,
+ * ...  Per chunk:
+ *   - with flags: an outlier iff r > thr[h] (r as in hqmq_encode, the given
+ *     threshold as in hqmq_outlier_extract_given_thr) and a slot of its
+ *     (page, head) is left: flag set, its values to fp16 (saturating), index
+ *     and radius 0.  Without a slot left it is coded like any other chunk and
+ *     the status gets HQMQ_FLAG_OUTLIER_OVERFLOW; n_outliers counts every
+ *     chunk above the threshold;
+ *   - radius and index as hqmq_encode; scores within fp32 rounding of each
+ *     other are compared in fp64, so the index is the argmax of the exact
+ *     scores (ties to the lowest index).
+ * The result does not depend on how tokens are split into calls.  Sequences
+ * must not share a page that this call writes.  k and v agree in page_size
+ * and heads; v may be NULL (d_xv is then ignored).  With search tables
+ * (hqmq_make_search_table) longer runs of tokens are searched through them.
+ * d_cu_tokens: int32 [n_seqs + 1], non-decreasing from 0 to n_tokens;
+ * d_pos0: int32 [n_seqs].  Data 16-byte aligned, strides multiples of 4
+ * elements (bf16) or 4 (fp32).  n_tokens may be 0 (nothing is done). */
+HQMQ_API int hqmq_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pages *v, const void *d_xk,
+                              const void *d_xv, int dtype, int64_t k_stride_t,
+                              int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                              int n_tokens, int n_seqs, const int32_t *d_cu_tokens,
+                              const int32_t *d_pos0, const int32_t *d_block_table, int max_pages,
+                              hqmq_status *d_status, void *stream);
+
+/* Reads pages back: d_y[b][h][t] ([n_seqs][heads][T][128] of out_dtype,
+ * 16-byte aligned) = the token at position t of sequence b, exactly as
+ * hqmq_decode gives it (r c rounded once; a flagged chunk its fp16 values;
+ * an index >= 24 S decodes to 0 and sets HQMQ_FLAG_BAD_INDEX).  Rows t >=
+ * d_seq_len[b] (clamped to [0, T]) and rows of bad pages are left as they
+ * are. */
+HQMQ_API int hqmq_paged_read(const hqmq_kv_pages *c, int n_seqs, const int32_t *d_seq_len,
+                             const int32_t *d_block_table, int max_pages, int T, void *d_y,
+                             int out_dtype, hqmq_status *d_status, void *stream);
+
+/* Bytes of device workspace of hqmq_attention_paged (partial results of the
+ * split token ranges); 0 for sizes the call rejects.  max_tokens = max_pages
+ * page_size. */
+HQMQ_API uint64_t hqmq_attention_paged_workspace_size(int B, int Hq, int Hk, int max_tokens,
+                                                      int prefix_len);
+
+/* Decode-phase attention over paged caches, one query token per sequence,
+ * with an optional prefix that all sequences share and that is decoded and
+ * multiplied once for all of them.  Sequence b attends to the prefix's
+ * prefix_len tokens (d_prefix_table, int32 [ceil(prefix_len / page_size)])
+ * and then to its own d_seq_len[b] tokens (its row of d_block_table):
+ *   o[b][h] = sum_t softmax_t(scale <q[b][h], K^_t>) V^_t,   KV head h / G,
+ * with K^, V^ the bf16 values of hqmq_paged_read and G = Hq / heads <= 16.
+ * bf16 products accumulated in fp32; softmax in base 2 with a running
+ * maximum; the weights enter P V as two bf16 terms.  No token at all gives
+ * o = 0 and lse = -inf; tokens of bad pages are left out.  d_seq_len is
+ * clamped to [0, max_pages page_size].
+ * d_lse: fp32 [B][Hq] or NULL, ln sum_t exp(scale <q, K^_t>), with which
+ * the result can be joined with attention over tokens held elsewhere.
+ * d_q: bf16 [B][Hq][128], 16-byte aligned; d_o: [B][Hq][128] of out_dtype,
+ * 16-byte aligned; d_block_table NULL with max_pages 0: the prefix alone.
+ * d_ws: at least hqmq_attention_paged_workspace_size bytes, 256-byte
+ * aligned, contents on entry ignored. */
+HQMQ_API int hqmq_attention_paged(const uint16_t *d_q, const hqmq_kv_pages *k,
+                                  const hqmq_kv_pages *v, int B, int Hq,
+                                  const int32_t *d_seq_len, const int32_t *d_block_table,
+                                  int max_pages, const int32_t *d_prefix_table, int prefix_len,
+                                  float scale, void *d_o, int out_dtype, float *d_lse, void *d_ws,
+                                  uint64_t ws_bytes, hqmq_status *d_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

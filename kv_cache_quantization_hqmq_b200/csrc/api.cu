@@ -117,6 +117,30 @@ extern "C" int hqmq_launch_encode_lut(const void *x, int dtype, int B, int H, in
                                       uint16_t *radius, hqmq_status *st, int sm_count,
                                       cudaStream_t stream);
 
+extern "C" int hqmq_launch_norm_rope(const hqmq_head_view *q, const hqmq_head_view *q_out,
+                                     const hqmq_head_view *k, const hqmq_head_view *k_out, int dtype,
+                                     int B, int T, int D, const void *qw, const void *kw, int w_dtype,
+                                     float eps, const int32_t *pos, const double *inv_freq, int R,
+                                     int interleaved, cudaStream_t stream);
+extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pages *v,
+                                       uint32_t bk, uint32_t bv, const void *xk, const void *xv,
+                                       int dtype, int64_t kst, int64_t ksh, int64_t vst, int64_t vsh,
+                                       int n_tokens, int n_seqs, const int32_t *cu,
+                                       const int32_t *pos0, const int32_t *table, int max_pages,
+                                       hqmq_status *st, cudaStream_t stream);
+extern "C" int hqmq_launch_paged_read(const hqmq_kv_pages *c, uint32_t b, int n_seqs,
+                                      const int32_t *len, const int32_t *table, int max_pages, int T,
+                                      void *y, int out_dtype, hqmq_status *st, cudaStream_t stream);
+extern "C" uint64_t hqmq_paged_attn_workspace_bytes(int B, int Hq, int Hk, int max_tokens,
+                                                    int prefix_len);
+extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_pages *k,
+                                           const hqmq_kv_pages *v, uint32_t bk, uint32_t bv, int B,
+                                           int Hq, const int32_t *seq_len, const int32_t *table,
+                                           int max_pages, const int32_t *prefix_table,
+                                           int prefix_len, float scale, void *o, int out_dtype,
+                                           float *lse, void *ws, hqmq_status *st,
+                                           cudaStream_t stream);
+
 namespace {
 
 constexpr uint32_t S_MAX = 65535;
@@ -180,6 +204,47 @@ int kv_codes_check(const hqmq_kv_codes *c) {
     if (!aligned(c->idx_words, 4) || !aligned(c->radius, 16) || !aligned(c->codebook, 16) ||
         !aligned(c->out_idx, 4) || !aligned(c->out_val, 8) || !aligned(c->tile_off, 4))
         return HQMQ_ERR_ALIGN;
+    return HQMQ_OK;
+}
+
+// A paged cache: geometry within its limits, pointers present and aligned.
+constexpr uint32_t PAGED_MAX_S = 48;
+constexpr int PAGED_MAX_HEADS = 1024;
+constexpr int PAGED_MAX_SEQS = 65535;         // grid z
+
+int kv_pages_check(const hqmq_kv_pages *p) {
+    if (!p || !p->idx_words || !p->radius || !p->codebook) return HQMQ_ERR_ARG;
+    if (p->S < 1 || p->S > PAGED_MAX_S || p->n_pages < 1) return HQMQ_ERR_ARG;
+    if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
+        return HQMQ_ERR_ARG;
+    if (p->heads < 1 || p->heads > PAGED_MAX_HEADS) return HQMQ_ERR_ARG;
+    if (p->flags && (!p->out_val || p->out_cap < 1 || p->out_cap > 32 * p->page_size))
+        return HQMQ_ERR_ARG;
+    if (!aligned(p->idx_words, 16) || !aligned(p->radius, 16) || !aligned(p->flags, 16) ||
+        !aligned(p->out_val, 16) || !aligned(p->codebook, 16) || !aligned(p->thr, 4) ||
+        !aligned(p->table, 16))
+        return HQMQ_ERR_ALIGN;
+    return HQMQ_OK;
+}
+
+// The block table's width: positions fit an int.
+bool table_ok(int max_pages, int page_size) {
+    return max_pages >= 0 && (int64_t)max_pages * page_size <= 0x7FFFFFFFll - 256;
+}
+
+bool paged_attention_sizes_ok(int B, int Hq, int Hk, int64_t max_tokens, int prefix_len) {
+    if (B < 1 || B > PAGED_MAX_SEQS || Hk < 1 || Hk > PAGED_MAX_HEADS) return false;
+    if (Hq < 1 || Hq % Hk != 0 || Hq / Hk > 16) return false;
+    return max_tokens >= 0 && max_tokens <= 0x7FFFFFFFll - 256 && prefix_len >= 0 &&
+           prefix_len <= 0x7FFFFFFF - 256;
+}
+
+// A strided tensor of hqmq_qk_norm_rope and its output.
+int head_views_check(const hqmq_head_view *in, const hqmq_head_view *out, int esz) {
+    if (!in && !out) return HQMQ_OK;
+    if (!in || !out || !in->data || !out->data) return HQMQ_ERR_ARG;
+    if (in->heads < 1 || in->heads != out->heads) return HQMQ_ERR_ARG;
+    if (!aligned(in->data, esz) || !aligned(out->data, esz)) return HQMQ_ERR_ALIGN;
     return HQMQ_OK;
 }
 
@@ -555,6 +620,110 @@ int hqmq_append_batch(const void *d_x, int dtype, int n_calls, int B, int H, int
                               hqmq_index_bits(S), d_idx_words, d_radius, d_out_idx, d_out_val,
                               d_slab_off, d_tile_off, (uint32_t)cap, d_status,
                               (cudaStream_t)stream);
+}
+
+int hqmq_qk_norm_rope(const hqmq_head_view *q, const hqmq_head_view *q_out,
+                      const hqmq_head_view *k, const hqmq_head_view *k_out, int dtype, int B, int T,
+                      int D, const void *d_q_weight, const void *d_k_weight, int w_dtype, float eps,
+                      const int32_t *d_pos, const double *d_inv_freq, int R, int interleaved,
+                      void *stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(w_dtype) || B < 0 || T < 0 || D < 1 || D > 512)
+        return HQMQ_ERR_ARG;
+    if (R < 0 || R > D || R % 2 != 0 || (R > 0 && !d_inv_freq)) return HQMQ_ERR_ARG;
+    if (!(eps >= 0.0f) || eps - eps != 0.0f) return HQMQ_ERR_ARG;
+    if ((!q && !k) || (uint64_t)B * (uint64_t)T > 0x7FFFFFFFull) return HQMQ_ERR_ARG;
+    if (B == 0 || T == 0) return HQMQ_OK;
+    const int esz = dtype == HQMQ_BF16 ? 2 : 4, wsz = w_dtype == HQMQ_BF16 ? 2 : 4;
+    int rc = head_views_check(q, q_out, esz);
+    if (rc == HQMQ_OK) rc = head_views_check(k, k_out, esz);
+    if (rc != HQMQ_OK) return rc;
+    if (!d_pos && R > 0) return HQMQ_ERR_ARG;
+    if (!aligned(d_pos, 4) || !aligned(d_inv_freq, 8) || !aligned(d_q_weight, wsz) ||
+        !aligned(d_k_weight, wsz))
+        return HQMQ_ERR_ALIGN;
+    return hqmq_launch_norm_rope(q, q_out, k, k_out, dtype, B, T, D, d_q_weight, d_k_weight,
+                                 w_dtype, eps, d_pos, d_inv_freq, R, interleaved,
+                                 (cudaStream_t)stream);
+}
+
+int hqmq_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pages *v, const void *d_xk,
+                     const void *d_xv, int dtype, int64_t k_stride_t, int64_t k_stride_h,
+                     int64_t v_stride_t, int64_t v_stride_h, int n_tokens, int n_seqs,
+                     const int32_t *d_cu_tokens, const int32_t *d_pos0,
+                     const int32_t *d_block_table, int max_pages, hqmq_status *d_status,
+                     void *stream) {
+    int rc = kv_pages_check(k);
+    if (rc == HQMQ_OK && v) rc = kv_pages_check(v);
+    if (rc != HQMQ_OK) return rc;
+    if (!dtype_ok(dtype) || n_tokens < 0 || n_seqs < 1 || n_seqs > PAGED_MAX_SEQS)
+        return HQMQ_ERR_ARG;
+    if (v && (v->page_size != k->page_size || v->heads != k->heads)) return HQMQ_ERR_ARG;
+    if ((k->flags && !k->thr) || (v && v->flags && !v->thr)) return HQMQ_ERR_ARG;
+    if (max_pages < 1 || !table_ok(max_pages, k->page_size)) return HQMQ_ERR_ARG;
+    if (n_tokens == 0) return HQMQ_OK;
+    if (!d_xk || (v && !d_xv) || !d_cu_tokens || !d_pos0 || !d_block_table) return HQMQ_ERR_ARG;
+    if (!aligned(d_xk, 16) || (v && !aligned(d_xv, 16)) || !aligned(d_cu_tokens, 4) ||
+        !aligned(d_pos0, 4) || !aligned(d_block_table, 4) || !aligned(d_status, 8))
+        return HQMQ_ERR_ALIGN;
+    if (k_stride_t % 4 || k_stride_h % 4 || (v && (v_stride_t % 4 || v_stride_h % 4)))
+        return HQMQ_ERR_ALIGN;
+    return hqmq_launch_paged_write(k, v, hqmq_index_bits(k->S), v ? hqmq_index_bits(v->S) : 0,
+                                   d_xk, d_xv, dtype, k_stride_t, k_stride_h, v_stride_t,
+                                   v_stride_h, n_tokens, n_seqs, d_cu_tokens, d_pos0,
+                                   d_block_table, max_pages, d_status, (cudaStream_t)stream);
+}
+
+int hqmq_paged_read(const hqmq_kv_pages *c, int n_seqs, const int32_t *d_seq_len,
+                    const int32_t *d_block_table, int max_pages, int T, void *d_y, int out_dtype,
+                    hqmq_status *d_status, void *stream) {
+    const int rc = kv_pages_check(c);
+    if (rc != HQMQ_OK) return rc;
+    if (!dtype_ok(out_dtype) || n_seqs < 1 || n_seqs > PAGED_MAX_SEQS || T < 0)
+        return HQMQ_ERR_ARG;
+    if (max_pages < 1 || !table_ok(max_pages, c->page_size)) return HQMQ_ERR_ARG;
+    if (T == 0) return HQMQ_OK;
+    if (!d_seq_len || !d_block_table || !d_y) return HQMQ_ERR_ARG;
+    if (!aligned(d_seq_len, 4) || !aligned(d_block_table, 4) || !aligned(d_y, 16) ||
+        !aligned(d_status, 8))
+        return HQMQ_ERR_ALIGN;
+    return hqmq_launch_paged_read(c, hqmq_index_bits(c->S), n_seqs, d_seq_len, d_block_table,
+                                  max_pages, T, d_y, out_dtype, d_status, (cudaStream_t)stream);
+}
+
+uint64_t hqmq_attention_paged_workspace_size(int B, int Hq, int Hk, int max_tokens,
+                                             int prefix_len) {
+    if (!paged_attention_sizes_ok(B, Hq, Hk, max_tokens, prefix_len)) return 0;
+    return hqmq_paged_attn_workspace_bytes(B, Hq, Hk, max_tokens, prefix_len);
+}
+
+int hqmq_attention_paged(const uint16_t *d_q, const hqmq_kv_pages *k, const hqmq_kv_pages *v, int B,
+                         int Hq, const int32_t *d_seq_len, const int32_t *d_block_table,
+                         int max_pages, const int32_t *d_prefix_table, int prefix_len, float scale,
+                         void *d_o, int out_dtype, float *d_lse, void *d_ws, uint64_t ws_bytes,
+                         hqmq_status *d_status, void *stream) {
+    int rc = kv_pages_check(k);
+    if (rc == HQMQ_OK) rc = kv_pages_check(v);
+    if (rc != HQMQ_OK) return rc;
+    if (v->page_size != k->page_size || v->heads != k->heads || !dtype_ok(out_dtype))
+        return HQMQ_ERR_ARG;
+    if (!table_ok(max_pages, k->page_size)) return HQMQ_ERR_ARG;
+    if (!paged_attention_sizes_ok(B, Hq, k->heads, (int64_t)max_pages * k->page_size, prefix_len))
+        return HQMQ_ERR_ARG;
+    if (!(scale == scale) || scale - scale != 0.0f) return HQMQ_ERR_ARG;
+    if (!d_q || !d_o || !d_ws) return HQMQ_ERR_ARG;
+    if (max_pages > 0 && (!d_seq_len || !d_block_table)) return HQMQ_ERR_ARG;
+    if (prefix_len > 0 && !d_prefix_table) return HQMQ_ERR_ARG;
+    if (!aligned(d_q, 16) || !aligned(d_o, 16) || !aligned(d_seq_len, 4) ||
+        !aligned(d_block_table, 4) || !aligned(d_prefix_table, 4) || !aligned(d_lse, 4) ||
+        !aligned(d_ws, 256) || !aligned(d_status, 8))
+        return HQMQ_ERR_ALIGN;
+    if (ws_bytes < hqmq_paged_attn_workspace_bytes(B, Hq, k->heads, max_pages * k->page_size,
+                                                   prefix_len))
+        return HQMQ_ERR_WORKSPACE;
+    return hqmq_launch_attention_paged(d_q, k, v, hqmq_index_bits(k->S), hqmq_index_bits(v->S), B,
+                                       Hq, d_seq_len, d_block_table, max_pages, d_prefix_table,
+                                       prefix_len, scale, d_o, out_dtype, d_lse, d_ws, d_status,
+                                       (cudaStream_t)stream);
 }
 
 }  // extern "C"

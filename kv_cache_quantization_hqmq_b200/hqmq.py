@@ -25,6 +25,18 @@ A serving flow, per (layer, role) cache x [B, H, T, 128] (bf16):
     hqmq_attention_decode(q, k, v, S, H, T, o, alloc_attention_ws(B, H), seq_len=lens)
     # or the dense cache: hqmq_decode(words, radius, cb_call, S, out_idx, out_val,
     #                                  slab_off, cap, 0, y, tile_off=tile_off)
+
+The same over pages, for caches that grow and share prefixes (once per layer):
+
+    words, radius, flags, val = alloc_kv_pages(n_pages, H, 64, S, out_cap=128)
+    kp = kv_pages(words, radius, cb_k, flags, val, thr_k, table_k)     # vp likewise
+    ws = alloc_attention_paged_ws(B, Hq, kp, max_pages, prefix_len)
+    # every step: queries and keys normed and rotated, K and V quantised into the pages
+    hqmq_qk_norm_rope(q, k, q, k, pos, rope_inv_freq(128, 500000.0), q_weight, k_weight)
+    hqmq_paged_write(k_new, v_new, kp, vp, block_table, cu_tokens, pos0)
+    hqmq_attention_paged(q_new, kp, vp, block_table, seq_len, o, ws,
+                         prefix_table=prefix_table, prefix_len=prefix_len)
+    # or the dense tokens: hqmq_paged_read(kp, block_table, seq_len, y)
 """
 from __future__ import annotations
 
@@ -41,6 +53,7 @@ HQMQ_BF16, HQMQ_F32 = 0, 1
 HQMQ_GRAN_CHUNK, HQMQ_GRAN_ELEMENT = 0, 1
 FLAG_OUTLIER_OVERFLOW, FLAG_SATURATED, FLAG_NONFINITE, FLAG_BAD_INDEX = 1, 2, 4, 8
 FLAG_MED3_FALLBACK = 16
+FLAG_BAD_PAGE = 32
 
 
 class HQMQError(RuntimeError):
@@ -55,6 +68,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _P, _I, _U32, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float
+_I64 = ctypes.c_int64
 _SIGS = {
     "hqmq_version": (ctypes.c_char_p, []),
     "hqmq_error_string": (ctypes.c_char_p, [_I]),
@@ -92,6 +106,13 @@ _SIGS = {
     "hqmq_attention_workspace_size": (_U64, [_I, _I]),
     "hqmq_attention_decode": (_I, [_P, _P, _P, _P, _U32, _I, _I, _I, _I, _I, _F, _P, _I, _P,
                                    _U64, _P, _P]),
+    "hqmq_qk_norm_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _F, _P, _P, _I, _I, _P]),
+    "hqmq_paged_write": (_I, [_P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I, _P, _P, _P, _I,
+                              _P, _P]),
+    "hqmq_paged_read": (_I, [_P, _I, _P, _P, _I, _I, _P, _I, _P, _P]),
+    "hqmq_attention_paged_workspace_size": (_U64, [_I, _I, _I, _I, _I]),
+    "hqmq_attention_paged": (_I, [_P, _P, _P, _I, _I, _P, _P, _I, _P, _I, _F, _P, _I, _P, _P, _U64,
+                                  _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -377,6 +398,232 @@ def hqmq_attention_decode(q, k, v, S, Hk, T, o, ws, scale=None, seq_len=None, st
 
 def alloc_attention_ws(B, Hk, device="cuda"):
     return torch.empty(hqmq_attention_workspace_size(B, Hk), dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------- paged cache
+def _here(*tensors):
+    """The tensors are on the current CUDA device (the calls launch there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("tensors must be on the current CUDA device %d, got one on %s "
+                             "(call under torch.cuda.device)" % (dev, t.device))
+
+
+def _ints(name, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s, got %s %s"
+                         % (name, shape, t.dtype, tuple(t.shape)))
+
+
+def _table(t, n_seqs, name="block_table"):
+    if t.dim() != 2 or t.shape[0] != n_seqs:
+        raise ValueError("%s must be [%d, max_pages], got %s" % (name, n_seqs, tuple(t.shape)))
+    _ints(name, t, tuple(t.shape))
+    return t.shape[1]
+
+
+class KVPages(ctypes.Structure):
+    """hqmq_kv_pages: a paged coded K or V cache (device pointers)."""
+    _fields_ = [("idx_words", _P), ("radius", _P), ("flags", _P), ("out_val", _P),
+                ("codebook", _P), ("thr", _P), ("table", _P), ("S", _U32), ("n_pages", _I),
+                ("page_size", _I), ("heads", _I), ("out_cap", _I)]
+
+
+def alloc_kv_pages(n_pages, heads, page_size, S, out_cap=0, device="cuda"):
+    """(idx_words, radius, flags, out_val) of an empty pool: int32 [n_pages, heads, page_size, b],
+    fp16 bits as int16 [..., 32], int32 [n_pages, heads, page_size] and int16 [n_pages, heads,
+    out_cap, 4]; the last two None if out_cap is 0 (no outliers)."""
+    words = torch.zeros(n_pages, heads, page_size, hqmq_index_bits(S), dtype=torch.int32, device=device)
+    radius = torch.zeros(n_pages, heads, page_size, 32, dtype=torch.int16, device=device)
+    if not out_cap:
+        return words, radius, None, None
+    flags = torch.zeros(n_pages, heads, page_size, dtype=torch.int32, device=device)
+    out_val = torch.zeros(n_pages, heads, out_cap, 4, dtype=torch.int16, device=device)
+    return words, radius, flags, out_val
+
+
+def kv_pages(idx_words, radius, codebook, flags=None, out_val=None, thr=None, table=None):
+    """The hqmq_kv_pages record of one paged cache (the tensors must outlive the
+    calls that use it), shapes as alloc_kv_pages gives them; codebook: fp32
+    [heads, S, 4]; thr: fp32 [heads] (to write with flags); table: the search
+    tables of the heads' codebooks or None."""
+    if codebook.dim() != 3 or codebook.shape[2] != 4:
+        raise ValueError("codebook must be fp32 [heads, S, 4]")
+    heads, S = int(codebook.shape[0]), int(codebook.shape[1])
+    b = hqmq_index_bits(S)
+    if idx_words.dim() != 4 or idx_words.shape[1] != heads or idx_words.shape[3] != b:
+        raise ValueError("idx_words must be [n_pages, %d, page_size, %d], got %s"
+                         % (heads, b, tuple(idx_words.shape)))
+    n_pages, _, P, _ = (int(v) for v in idx_words.shape)
+    if (flags is None) != (out_val is None):
+        raise ValueError("flags and out_val come together")
+    cap = int(out_val.shape[2]) if out_val is not None and out_val.dim() == 4 else 0
+    want = (("idx_words", idx_words, (n_pages, heads, P, b), 4),
+            ("radius", radius, (n_pages, heads, P, 32), 2),
+            ("flags", flags, (n_pages, heads, P), 4),
+            ("out_val", out_val, (n_pages, heads, cap, 4), 2),
+            ("codebook", codebook, (heads, S, 4), 4), ("thr", thr, (heads,), 4))
+    for name, t, shape, size in want:
+        if t is None and name in ("flags", "out_val", "thr"):
+            continue
+        if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous():
+            raise ValueError("%s must be contiguous %s of %d-byte elements, got %s %s"
+                             % (name, shape, size, t.dtype, tuple(t.shape)))
+    if codebook.dtype != torch.float32 or (thr is not None and thr.dtype != torch.float32):
+        raise ValueError("codebook and thr are fp32")
+    if table is not None and (not hqmq_search_table_bytes(S) or not table.is_contiguous() or
+                              table.numel() * table.element_size() < heads * hqmq_search_table_bytes(S)):
+        raise ValueError("table must hold the search tables of %d heads" % heads)
+    _here(idx_words, radius, flags, out_val, codebook, thr, table)
+    c = KVPages(_ptr(idx_words), _ptr(radius), _ptr(flags), _ptr(out_val), _ptr(codebook), _ptr(thr),
+                _ptr(table), S, n_pages, P, heads, cap)
+    c._keep = (idx_words, radius, flags, out_val, codebook, thr, table)
+    return c
+
+
+class _HeadView(ctypes.Structure):
+    _fields_ = [("data", _P), ("stride_b", _I64), ("stride_t", _I64), ("stride_h", _I64), ("heads", _I)]
+
+
+def _head_view(x):
+    sb, st, sh, sd = x.stride()
+    if sd != 1 and x.shape[3] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return _HeadView(x.data_ptr(), sb, st, sh, x.shape[2])
+
+
+def rope_inv_freq(R, base=10000.0, device="cuda"):
+    """fp64 [R / 2] of base^(-2 i / R), the d_inv_freq of hqmq_qk_norm_rope."""
+    return base ** -(torch.arange(0, R, 2, dtype=torch.float64, device=device) / R)
+
+
+def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                      interleaved=False, stream=None):
+    """RMS norm (where a weight is given) of every head vector of q [B, T, Hq, D] and
+    k [B, T, Hk, D] and the rotation of its first 2 len(inv_freq) elements by
+    pos [B, T] (int32) * inv_freq (fp64, or None), into q_out and k_out: the same
+    shapes, strides of their own (q_out may be q).  q or k may be None."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 4:
+        raise ValueError("q and k are [B, T, heads, D]")
+    B, T, _, D = x.shape
+    for t, t_out, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
+        if t is None:
+            if t_out is not None or w is not None:
+                raise ValueError("an output or weight without its input")
+            continue
+        if t_out is None or t.dim() != 4 or t.shape[:2] != (B, T) or t.shape[3] != D or \
+                t_out.shape != t.shape or t.dtype != x.dtype or t_out.dtype != x.dtype:
+            raise ValueError("q, k and their outputs must agree in B, T, D and dtype")
+        if w is not None and (tuple(w.shape) != (D,) or not w.is_contiguous()):
+            raise ValueError("weights are contiguous [D]")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("the weights must have one dtype")
+    R = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous fp64 vector")
+        R = 2 * inv_freq.shape[0]
+        _ints("pos", pos, (B, T))
+    w = q_weight if q_weight is not None else k_weight
+    _here(q, k, q_out, k_out, pos, inv_freq, q_weight, k_weight)
+    views = [None if t is None else ctypes.byref(_head_view(t)) for t in (q, q_out, k, k_out)]
+    _check("hqmq_qk_norm_rope", _lib.hqmq_qk_norm_rope(
+        *views, _dtype_code(x), B, T, D, _ptr(q_weight), _ptr(k_weight),
+        HQMQ_BF16 if w is None else _dtype_code(w), float(eps), _ptr(pos), _ptr(inv_freq), R,
+        1 if interleaved else 0, _stream(stream)))
+
+
+def _new_tokens(x, heads):
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128 or x.stride(2) != 1:
+        raise ValueError("new tokens are [n_tokens, %d, 128] with a contiguous last dimension, got "
+                         "%s" % (heads, tuple(x.shape)))
+
+
+def hqmq_paged_write(xk, xv, k, v, block_table, cu_tokens, pos0, status=None, stream=None):
+    """Quantises new tokens xk, xv ([n_tokens, heads, 128], bf16 or fp32, any token
+    and head strides) into the pages k, v (KVPages): sequence b's are rows
+    cu_tokens[b] .. cu_tokens[b+1]-1 and go to positions pos0[b], pos0[b]+1, ...
+    block_table: int32 [n_seqs, max_pages]; cu_tokens: int32 [n_seqs + 1]; pos0:
+    int32 [n_seqs].  xv and v may be None."""
+    _new_tokens(xk, k.heads)
+    vs = (0, 0)
+    if v is not None:
+        _new_tokens(xv, v.heads)
+        if xv.shape != xk.shape or xv.dtype != xk.dtype:
+            raise ValueError("xk and xv must agree in shape and dtype")
+        vs = xv.stride()
+    n_seqs = pos0.shape[0] if pos0.dim() == 1 else -1
+    _ints("pos0", pos0, (n_seqs,))
+    _ints("cu_tokens", cu_tokens, (n_seqs + 1,))
+    max_pages = _table(block_table, n_seqs)
+    _here(xk, xv, k._keep[0], None if v is None else v._keep[0], block_table, cu_tokens, pos0, status)
+    _check("hqmq_paged_write", _lib.hqmq_paged_write(
+        ctypes.byref(k), None if v is None else ctypes.byref(v), _ptr(xk),
+        None if v is None else _ptr(xv), _dtype_code(xk), xk.stride(0), xk.stride(1), vs[0], vs[1],
+        xk.shape[0], n_seqs, _ptr(cu_tokens), _ptr(pos0), _ptr(block_table), max_pages,
+        _ptr(status), _stream(stream)))
+
+
+def hqmq_paged_read(c, block_table, seq_len, y, status=None, stream=None):
+    """y[b, h, t] (contiguous [n_seqs, heads, T, 128], bf16 or fp32) = the token at
+    position t < seq_len[b] of sequence b; the other rows are left as they are."""
+    B, H, T, D = _shape4(y)
+    if H != c.heads or D != 128:
+        raise ValueError("y must be [n_seqs, %d, T, 128]" % c.heads)
+    _ints("seq_len", seq_len, (B,))
+    max_pages = _table(block_table, B)
+    _here(c._keep[0], block_table, seq_len, y, status)
+    _check("hqmq_paged_read", _lib.hqmq_paged_read(
+        ctypes.byref(c), B, _ptr(seq_len), _ptr(block_table), max_pages, T, _ptr(y), _dtype_code(y),
+        _ptr(status), _stream(stream)))
+    return y
+
+
+def hqmq_attention_paged_workspace_size(B, Hq, Hk, max_tokens, prefix_len=0):
+    return int(_lib.hqmq_attention_paged_workspace_size(B, Hq, Hk, max_tokens, prefix_len))
+
+
+def alloc_attention_paged_ws(B, Hq, k, max_pages, prefix_len=0, device="cuda"):
+    """Workspace of hqmq_attention_paged over pages like k (KVPages)."""
+    n = hqmq_attention_paged_workspace_size(B, Hq, k.heads, max_pages * k.page_size, prefix_len)
+    if n == 0:
+        raise ValueError("sizes that hqmq_attention_paged does not take")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def hqmq_attention_paged(q, k, v, block_table, seq_len, o, ws, prefix_table=None, prefix_len=0,
+                         scale=None, lse=None, status=None, stream=None):
+    """o[b, h] = softmax(scale q[b, h] K^T) V over the prefix's prefix_len tokens
+    (prefix_table: int32 pages, shared by the batch and processed once for it)
+    and the seq_len[b] tokens of sequence b's row of block_table (None: the
+    prefix alone).  q: bf16 [B, Hq, 128]; o: bf16 or fp32 [B, Hq, 128]; lse:
+    fp32 [B, Hq] or None; scale defaults to 1/sqrt(128)."""
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [B, Hq, 128] tensor")
+    B, Hq, D = q.shape
+    if D != 128 or o.shape != q.shape or not o.is_contiguous():
+        raise ValueError("q and o are contiguous [B, Hq, 128]")
+    max_pages = 0
+    if block_table is not None:
+        max_pages = _table(block_table, B)
+        _ints("seq_len", seq_len, (B,))
+    if prefix_len > 0:
+        need = (prefix_len + k.page_size - 1) // k.page_size
+        if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
+            raise ValueError("prefix_table must hold the prefix's %d pages" % need)
+        _ints("prefix_table", prefix_table, tuple(prefix_table.shape))
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [B, Hq] tensor")
+    _here(q, k._keep[0], v._keep[0], block_table, seq_len, o, ws, prefix_table, lse, status)
+    _check("hqmq_attention_paged", _lib.hqmq_attention_paged(
+        _ptr(q), ctypes.byref(k), ctypes.byref(v), B, Hq, _ptr(seq_len), _ptr(block_table), max_pages,
+        _ptr(prefix_table), int(prefix_len), D ** -0.5 if scale is None else float(scale), _ptr(o),
+        _dtype_code(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
+        _stream(stream)))
+    return o
 
 
 # ---------------------------------------------------------------- buffers
