@@ -533,6 +533,10 @@ typedef struct {
  * block table's last page: the tokens concerned are left out. */
 #define HQMQ_FLAG_BAD_PAGE 32u
 
+/* A bounded wait inside hqmq_attention_paged ran out (the outputs are then
+ * undefined); not seen on working hardware. */
+#define HQMQ_FLAG_TIMEOUT 64u
+
 /* One strided tensor [B][T][heads][D] whose last dimension is contiguous;
  * strides in elements. */
 typedef struct {

@@ -53,7 +53,7 @@ HQMQ_BF16, HQMQ_F32 = 0, 1
 HQMQ_GRAN_CHUNK, HQMQ_GRAN_ELEMENT = 0, 1
 FLAG_OUTLIER_OVERFLOW, FLAG_SATURATED, FLAG_NONFINITE, FLAG_BAD_INDEX = 1, 2, 4, 8
 FLAG_MED3_FALLBACK = 16
-FLAG_BAD_PAGE = 32
+FLAG_BAD_PAGE, FLAG_TIMEOUT = 32, 64
 
 
 class HQMQError(RuntimeError):
