@@ -20,7 +20,7 @@
 //     head's codeword table in shared memory into bf16 tiles [32 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
-//   * one thread issues the products (tcgen05.mma, 128 rows, accumulators
+//   * one warp's elected thread issues the products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
 //     softmax in base 2, P back as two bf16 terms P_hi + P_lo (about 16
@@ -45,8 +45,9 @@ constexpr int PA_MIN_TILES = 2;               // fewest tiles worth a CTA
 constexpr int PA_REP_ROWS = 32;               // segments up to this many rows are replicated
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
-constexpr int MASK_RING = 8;
-constexpr int PROD_WARPS = 8;
+constexpr int META_RING = 4;                  // tiles
+constexpr int MASK_RING = 16;                 // the scout is at most 12 tiles ahead of the softmax
+constexpr int PROD_WARPS = 16;
 
 struct PagedAttnArgs {
     const uint16_t *q;
@@ -144,27 +145,39 @@ template <int MT> struct Rows {
     __device__ __forceinline__ int groups() const { return rep ? 1 : (n + 127) / 128; }
 };
 
+// What the scout warp finds out about a tile.
+struct Meta {
+    long long page[2];                        // page * heads + head of its halves (16 tokens)
+    int row0, head;                           // row of the first token in its page
+    uint32_t mask;                            // valid tokens
+    uint32_t flags[2][PA_TILE];               // flag words of K and V
+    uint16_t start[2][PA_TILE];               // slots of their first values
+};
+
 template <int MT> struct Shared {
     static constexpr int NB = MT == 1 ? 2 : 1;          // S and P buffers of a group
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full[MT], s_full[MT][NB], s_empty[MT][NB], p_full[MT][NB], p_empty[MT][NB];
+    uint64_t meta_full[META_RING], meta_empty[META_RING];
     uint64_t heads;                                     // the producers, at a change of heads
     uint64_t drain;
+    Meta meta[META_RING];
     uint32_t mask[MASK_RING];                           // valid tokens of the last tiles
     Cursor start;
+    int last_head;                                      // of the share
     uint32_t tmem;
     int failed;
 };
 
 // Tensor memory columns: O and Q of every group, then its S and P buffers.
-template <int MT> struct Tmem {
+template <int MT, int NT> struct Tmem {
     static constexpr int NB = Shared<MT>::NB;
     static constexpr uint32_t COLS = 512;
     __device__ __forceinline__ static uint32_t o(int g) { return g * 128; }
     __device__ __forceinline__ static uint32_t q(int g) { return MT * 128 + g * 64; }
     __device__ __forceinline__ static uint32_t s(int g, int i) { return MT * 192 + (g * NB + i) * 32; }
-    __device__ __forceinline__ static uint32_t p(int g, int i) { return MT * 192 + (MT * NB + g * NB + i) * 32; }
-    static_assert(MT * 192 + 2 * MT * NB * 32 <= 512, "tensor memory");
+    __device__ __forceinline__ static uint32_t p(int g, int i) { return MT * 192 + MT * NB * 32 + (g * NB + i) * 16 * NT; }
+    static_assert(MT * 192 + MT * NB * (32 + 16 * NT) <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -192,6 +205,122 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------
+// scout: one warp, lane = token of the tile
+// ---------------------------------------------------------------------------
+// Page ids are fetched four tiles before the tile is handed on, flag words two.
+struct Scout {
+    const PagedAttnArgs &a;
+    const int lane;
+    Cursor c;
+    bool first;                               // the cursor's tile is the first of a piece
+    int len;                                  // tokens of its segment
+    const int *tab;                           // and its pages
+    uint32_t base;                            // flagged chunks before the next tile in its page, K | V << 16
+
+    struct Tile {
+        int head, t0, page;
+        bool first;
+        uint32_t fk, fv;
+    };
+
+    __device__ __forceinline__ Scout(const PagedAttnArgs &a_, const Cursor &c_, int lane_)
+        : a(a_), lane(lane_), c(c_), first(true), base(0) { segment(); }
+    __device__ __forceinline__ void segment() {
+        const bool pre = c.prefix(a);
+        const int b = c.seg - a.row_tiles;
+        len = c.left <= 0 ? 0 : pre ? a.prefix_len : own_len(a, b);
+        tab = pre ? a.prefix_table : a.table + (size_t)b * a.max_pages;
+    }
+
+    __device__ __forceinline__ void pages(Tile &x) {
+        x.head = -1;
+        if (c.left <= 0) return;
+        x.head = c.head;
+        x.t0 = c.tile * PA_TILE;
+        x.first = first;
+        x.page = -2;                          // no token
+        if (x.t0 + lane < len) x.page = __ldg(tab + ((x.t0 + lane) >> a.k.page_shift));
+        --c.left;
+        first = ++c.tile >= c.n_tiles;
+        if (first) {
+            c.settle(a);
+            segment();
+        }
+    }
+    __device__ __forceinline__ void flags(Tile &x) {
+        x.fk = x.fv = 0u;
+        if (x.head < 0) return;
+        if (x.page != -2 && (x.page < 0 || x.page >= a.k.n_pages || x.page >= a.v.n_pages)) {
+            if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
+            x.page = -1;
+        }
+        if (x.page >= 0) {
+            const size_t at = a.k.at(x.page, x.head, (x.t0 + lane) & (a.k.page_size - 1));
+            if (a.k.flags) x.fk = __ldg(a.k.flags + at);
+            if (a.v.flags) x.fv = __ldg(a.v.flags + at);
+        }
+    }
+    __device__ __forceinline__ void hand_on(const Tile &x, Meta &m, uint32_t *mask) {
+        const int row0 = x.t0 & (a.k.page_size - 1);
+        if (row0 == 0) base = 0;
+        else if (x.first) {                   // a piece that starts inside a page
+            const int pg = __shfl_sync(FULL, x.page, 0);
+            const size_t f = pg >= 0 ? a.k.at(pg, x.head, 0) : 0;
+            base = pg >= 0 && a.k.flags ? flags_before(a.k.flags + f, row0, lane) : 0u;
+            if (pg >= 0 && a.v.flags) base |= flags_before(a.v.flags + f, row0, lane) << 16;
+        }
+        const uint32_t n = __popc(x.fk) | (__popc(x.fv) << 16);
+        uint32_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += u;
+        }
+        uint32_t start = base + inc - n;
+        const uint32_t half = __shfl_sync(FULL, inc - n, 16);
+        if (a.k.page_size == 16 && lane >= 16) start -= half;
+        base += __shfl_sync(FULL, inc, 31);
+        const uint32_t ok = __ballot_sync(FULL, x.page >= 0);
+        m.flags[0][lane] = x.fk;
+        m.flags[1][lane] = x.fv;
+        m.start[0][lane] = (uint16_t)start;
+        m.start[1][lane] = (uint16_t)(start >> 16);
+        if ((lane & 15) == 0) m.page[lane >> 4] = (long long)x.page * a.k.heads + x.head;
+        if (lane == 0) {
+            m.row0 = row0;
+            m.head = x.head;
+            m.mask = ok;
+            *mask = ok;
+        }
+    }
+};
+
+template <int MT>
+__device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int lane) {
+    Scout s(a, sh.start, lane);
+    const int total = sh.start.left;
+    Scout::Tile x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.pages(x[i]);
+    s.flags(x[0]);
+    s.flags(x[1]);
+    for (int n = 0; n < total; n += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (n + i >= total) break;
+            const int slot = (n + i) % META_RING, use = (n + i) / META_RING;
+            s.flags(x[(i + 2) & 3]);
+            if (use > 0 && !mbar_wait(&sh.meta_empty[slot], (use - 1) & 1)) return false;
+            s.hand_on(x[i], sh.meta[slot], &sh.mask[(n + i) % MASK_RING]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.meta_full[slot]);
+            s.pages(x[i]);
+        }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
 
@@ -203,7 +332,7 @@ template <int R> __host__ __device__ constexpr uint32_t table_bytes(uint32_t S) 
 template <int R>
 __device__ __forceinline__ void build_table(const PagesDev &p, int head, uint32_t base, int thread) {
     const uint32_t n = 24u * p.S;
-    for (uint32_t e = thread; e <= n; e += 128) {
+    for (uint32_t e = thread; e <= n; e += PROD_WARPS * 16) {
         float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
         if (e < n) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
 #pragma unroll
@@ -216,110 +345,45 @@ __device__ __forceinline__ void build_table(const PagesDev &p, int head, uint32_
 // Words that hold a lane's 8 indices (bits 8 q b .. 8 q b + 8 b - 1).
 template <int BT> struct RunWords { static constexpr int N = BT == 8 ? 2 : BT == 10 ? 3 : 4; };
 
-// One tile on its way: lane (q, token) = (lane / 8, 8 sub + lane % 8) decodes
-// chunks 8 q .. 8 q + 7 of that token; for the flags lane = token.
+// One tile's codes on their way: lane (q, token) = (lane / 8, 8 sub + lane %
+// 8) decodes chunks 8 q .. 8 q + 7 of that token.
 template <int BT> struct Slot {
-    int t0, head;                             // tile whose page ids are under way
-    bool first;                               // first tile of a piece
-    int page;                                 // raw page id of token t0 + lane
-    int d_t0, d_head;                         // tile whose codes are under way
-    bool d_first;
-    int d_page, l_page;                       // page of the decoded token, of token t0 + lane
+    int head;
     uint4 rad;
     uint32_t w[RunWords<BT>::N];
-    uint32_t flags;                           // of token t0 + lane
-    uint32_t mask;                            // valid tokens
     uint32_t f8;                              // flagged chunks among this lane's
     int slot;                                 // slot of the first of them
     uint2 val;                                // and its value
+    const uint2 *slots;
 };
 
 template <int BT, int R> struct Producer {
-    const PagedAttnArgs &a;
     const PagesDev &p;
-    const int lane, sub, q;
-    const bool is_k;
-    int base;                                 // flagged chunks before the next tile of the page
+    const int lane, q, tok, which;
 
-    __device__ __forceinline__ Producer(const PagedAttnArgs &a_, bool k, int sub_, int lane_)
-        : a(a_), p(k ? a_.k : a_.v), lane(lane_), sub(sub_), q(lane_ >> 3), is_k(k), base(0) {}
+    __device__ __forceinline__ Producer(const PagesDev &p_, int which_, int sub, int lane_)
+        : p(p_), lane(lane_), q(lane_ >> 3), tok(sub * 8 + (lane_ & 7)), which(which_) {}
 
-    // Page ids of the cursor's tile.
-    __device__ __forceinline__ void fetch_pages(Slot<BT> &s, Cursor &c, bool &first) {
-        s.head = -1;
-        if (c.left <= 0) return;
-        s.head = c.head;
-        s.t0 = c.tile * PA_TILE;
-        s.first = first;
-        const bool pre = c.prefix(a);
-        const int b = c.seg - a.row_tiles;
-        const int len = pre ? a.prefix_len : own_len(a, b);
-        const int *tab = pre ? a.prefix_table : a.table + (size_t)b * a.max_pages;
-        const int t = s.t0 + lane;
-        s.page = -2;                          // no token
-        if (t < len) s.page = __ldg(tab + (t >> p.page_shift));
-        const int seg = c.seg, head = c.head;
-        c.skip(a, 1);
-        first = c.seg != seg || c.head != head;
-    }
-
-    // Codes of the tile whose page ids have arrived.
-    __device__ __forceinline__ void fetch_codes(Slot<BT> &s) {
-        s.d_head = s.head;
-        if (s.head < 0) return;
-        s.d_t0 = s.t0;
-        s.d_first = s.first;
-        int pg = s.page;
-        if (pg != -2 && (pg < 0 || pg >= a.k.n_pages || pg >= a.v.n_pages)) {
-            if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
-            pg = -1;
-        }
-        s.mask = __ballot_sync(FULL, pg >= 0);
-        s.l_page = pg;
-        s.d_page = __shfl_sync(FULL, pg, sub * 8 + (lane & 7));
+    __device__ __forceinline__ void fetch(Slot<BT> &s, const Meta &m) {
+        s.head = m.head;
         s.rad = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < RunWords<BT>::N; ++i) s.w[i] = 0u;
-        if (s.d_page >= 0) {
-            const size_t at = p.at(s.d_page, s.head, (s.t0 + sub * 8 + (lane & 7)) & (p.page_size - 1));
-            s.rad = __ldg(reinterpret_cast<const uint4 *>(p.radius + at * PG_CHUNKS) + q);
-            const uint32_t *w = p.words + at * p.b;
-            const uint32_t wo = (8u * q * p.b) >> 5;
-#pragma unroll
-            for (int i = 0; i < RunWords<BT>::N; ++i)
-                if (BT || wo + i < p.b) s.w[i] = __ldg(w + wo + i);
-        }
-        s.flags = 0u;
-        if (p.flags && pg >= 0) s.flags = __ldg(p.flags + p.at(pg, s.head, (s.t0 + lane) & (p.page_size - 1)));
-    }
-
-    // Slots of the flagged chunks and the first value, once the flags are there.
-    __device__ __forceinline__ void fetch_values(Slot<BT> &s) {
         s.f8 = 0u;
-        if (s.d_head < 0 || !p.flags) return;
-        const int row = (s.d_t0 + lane) & (p.page_size - 1);
-        const int row0 = __shfl_sync(FULL, row, 0);
-        if (row0 == 0) base = 0;
-        else if (s.d_first) {                 // a piece that starts inside a page
-            const int pg = __shfl_sync(FULL, s.l_page, 0);
-            base = pg >= 0 ? (int)flags_before(p.flags + p.at(pg, s.d_head, 0), row0, lane) : 0;
-        }
-        const int n = __popc(s.flags);
-        int inc = n;
+        if (!((m.mask >> tok) & 1u)) return;
+        const long long ph = m.page[tok >> 4];
+        const size_t at = ((size_t)ph << p.page_shift) + ((m.row0 + tok) & (p.page_size - 1));
+        s.rad = __ldg(reinterpret_cast<const uint4 *>(p.radius + at * PG_CHUNKS) + q);
+        const uint32_t b = BT ? BT : p.b, wo = (8u * q * b) >> 5;
+        const uint32_t *w = p.words + at * b + wo;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(FULL, inc, o);
-            if (lane >= o) inc += u;
-        }
-        int start = base + inc - n;
-        if (p.page_size == 16 && lane >= 16) start -= __shfl_sync(0xFFFF0000u, inc - n, 16);
-        base += __shfl_sync(FULL, inc, 31);
-        const int tok = sub * 8 + (lane & 7);
-        start = __shfl_sync(FULL, start, tok);
-        const uint32_t f = __shfl_sync(FULL, s.flags, tok);
+        for (int i = 0; i < RunWords<BT>::N; ++i)
+            if (BT || wo + i < b) s.w[i] = __ldg(w + i);
+        const uint32_t f = m.flags[which][tok];
         s.f8 = (f >> (8 * q)) & 0xFFu;
-        s.slot = start + __popc(f & ((1u << (8 * q)) - 1u));
-        if (s.f8 && s.slot < p.cap) s.val = __ldg(p.slots(s.d_page, s.d_head) + s.slot);
+        s.slot = m.start[which][tok] + __popc(f & ((1u << (8 * q)) - 1u));
+        s.slots = reinterpret_cast<const uint2 *>(p.val) + (size_t)ph * p.cap;
+        if (s.f8 && s.slot < p.cap) s.val = __ldg(s.slots + s.slot);
     }
 
     // The lane's 8 chunks to the tile, then the flagged ones over them.
@@ -332,52 +396,54 @@ template <int BT, int R> struct Producer {
             x[i] = BT == 8 ? s.w[i] : i + 1 < N ? __funnelshift_r(s.w[i], s.w[i + 1], sh) : s.w[i] >> sh;
         const uint32_t copy = (uint32_t)(lane & (R - 1)) * 16u;
         const uint32_t zero = ((24u * p.S) << LG) | copy;
-        const int tok = sub * 8 + (lane & 7);
         const uint32_t row = tile + (q >> 1) * (TILE_BYTES / 2) + (tok >> 3) * 1024 + (tok & 7) * 128;
         const uint32_t u0 = (q & 1) * 4, swz = tok & 7;
-        uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t v;                       // index << LG, other bits around it
-            if (BT) {
-                constexpr int BB = BT ? BT : 1;
-                const int pos = j * BB, wi = pos >> 5, s5 = pos & 31;
-                if (s5 + BB > 32 && wi + 1 < N) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5 - LG);
-                else v = s5 >= LG ? x[wi] >> (s5 - LG) : x[wi] << (LG - s5);
-            } else {
-                const uint32_t pos = j * b, wi = pos >> 5, s5 = pos & 31u;
-                uint32_t lo = x[0], hi = x[1];
+        for (int h = 0; h < 2; ++h) {
+            float4 c[4];
 #pragma unroll
-                for (int i = 1; i < N; ++i)
-                    if (wi == (uint32_t)i) {
-                        lo = x[i];
-                        hi = i + 1 < N ? x[i + 1] : 0u;
-                    }
-                v = __funnelshift_r(lo, hi, s5) << LG;
+            for (int k = 0; k < 4; ++k) {
+                const int j = 4 * h + k;
+                uint32_t v;                   // index << LG, other bits around it
+                if (BT) {
+                    constexpr int BB = BT ? BT : 1;
+                    const int pos = j * BB, wi = pos >> 5, s5 = pos & 31;
+                    if (s5 + BB > 32 && wi + 1 < N) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5 - LG);
+                    else v = s5 >= LG ? x[wi] >> (s5 - LG) : x[wi] << (LG - s5);
+                } else {
+                    const uint32_t pos = j * b, wi = pos >> 5, s5 = pos & 31u;
+                    uint32_t lo = x[0], hi = x[1];
+#pragma unroll
+                    for (int i = 1; i < N; ++i)
+                        if (wi == (uint32_t)i) {
+                            lo = x[i];
+                            hi = i + 1 < N ? x[i + 1] : 0u;
+                        }
+                    v = __funnelshift_r(lo, hi, s5) << LG;
+                }
+                c[k] = lds128(table + min((v & (((1u << b) - 1u) << LG)) | copy, zero));
             }
-            v = min((v & (((1u << b) - 1u) << LG)) | copy, zero);
-            const float4 c = lds128(table + v);
-            const uint32_t rw = j < 2 ? s.rad.x : j < 4 ? s.rad.y : j < 6 ? s.rad.z : s.rad.w;
-            const float r = f16_bits_to_f32((j & 1) ? rw >> 16 : rw & 0xFFFFu);
-            const float2 y01 = mul_pair(r, c.x, c.y), y23 = mul_pair(r, c.z, c.w);
-            o[2 * (j & 1)] = bf16x2(y01.x, y01.y);
-            o[2 * (j & 1) + 1] = bf16x2(y23.x, y23.y);
-            if (j & 1) sts128(row + ((u0 + (j >> 1)) ^ swz) * 16, o[0], o[1], o[2], o[3]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const uint32_t rw = h == 0 ? (k == 0 ? s.rad.x : s.rad.y) : (k == 0 ? s.rad.z : s.rad.w);
+                const float r0 = f16_bits_to_f32(rw & 0xFFFFu), r1 = f16_bits_to_f32(rw >> 16);
+                const float2 y0 = mul_pair(r0, c[k].x, c[k].y), y1 = mul_pair(r0, c[k].z, c[k].w);
+                const float2 y2 = mul_pair(r1, c[k + 1].x, c[k + 1].y), y3 = mul_pair(r1, c[k + 1].z, c[k + 1].w);
+                sts128(row + ((u0 + 2 * h + (k >> 1)) ^ swz) * 16, bf16x2(y0.x, y0.y), bf16x2(y1.x, y1.y),
+                       bf16x2(y2.x, y2.y), bf16x2(y3.x, y3.y));
+            }
         }
-        if (__any_sync(FULL, s.f8 != 0u)) {
-            uint32_t f8 = s.f8;
-            uint2 h = s.val;
-            int slot = s.slot;
-            while (f8) {
-                if (slot >= p.cap) break;
-                const int j = __ffs(f8) - 1;
-                f8 &= f8 - 1u;
-                sts64(row + ((u0 + (j >> 1)) ^ swz) * 16 + (j & 1) * 8,
-                      bf16x2(f16_bits_to_f32(h.x & 0xFFFFu), f16_bits_to_f32(h.x >> 16)),
-                      bf16x2(f16_bits_to_f32(h.y & 0xFFFFu), f16_bits_to_f32(h.y >> 16)));
-                ++slot;
-                if (f8 && slot < p.cap) h = __ldg(p.slots(s.d_page, s.d_head) + slot);
-            }
+        uint32_t f8 = s.f8;
+        uint2 v = s.val;
+        int slot = s.slot;
+        while (f8 && slot < p.cap) {
+            const int j = __ffs(f8) - 1;
+            f8 &= f8 - 1u;
+            sts64(row + ((u0 + (j >> 1)) ^ swz) * 16 + (j & 1) * 8,
+                  bf16x2(f16_bits_to_f32(v.x & 0xFFFFu), f16_bits_to_f32(v.x >> 16)),
+                  bf16x2(f16_bits_to_f32(v.y & 0xFFFFu), f16_bits_to_f32(v.y >> 16)));
+            ++slot;
+            if (f8 && slot < p.cap) v = __ldg(s.slots + slot);
         }
     }
 };
@@ -389,68 +455,74 @@ __device__ __forceinline__ bool meet(uint64_t &bar, int &times, int lane) {
     return mbar_wait(&bar, times++ & 1);
 }
 
+// Warps 0-7 take the even tiles, 8-15 the odd ones; of each eight, four K and
+// four V.  A tile's codes are fetched before the one before it is decoded.
 template <int BT, int R, int MT>
-__device__ __forceinline__ void produce(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tables, uint32_t tiles,
+__device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tables, uint32_t tiles,
                                         int warp, int lane) {
-    const bool is_k = warp < 4;
-    const int sub = warp & 3;
-    Producer<BT, R> pr(a, is_k, sub, lane);
-    const uint32_t table = tables + (is_k ? 0u : table_bytes<R>(a.k.S));
-    const uint32_t my_tiles = tiles + (is_k ? 0u : 2u * TILE_BYTES);
-    uint64_t *full = is_k ? sh.k_full : sh.v_full, *empty = is_k ? sh.k_empty : sh.v_empty;
-    Cursor c = sh.start;
-    const int total = c.left;
-    bool first = true;
-    Slot<BT> s[2];
-    pr.fetch_pages(s[0], c, first);
-    pr.fetch_pages(s[1], c, first);
-    pr.fetch_codes(s[0]);
-    pr.fetch_codes(s[1]);
-    pr.fetch_pages(s[0], c, first);
-    pr.fetch_pages(s[1], c, first);
-    pr.fetch_values(s[0]);
+    const int set = warp >> 3, which = (warp >> 2) & 1, sub = warp & 3;
+    Producer<BT, R> pr(which ? a.v : a.k, which, sub, lane);
+    const uint32_t table = tables + (which ? table_bytes<R>(a.k.S) : 0u);
+    const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u) + set * TILE_BYTES;
+    uint64_t *full = (which ? sh.v_full : sh.k_full) + set, *empty = (which ? sh.v_empty : sh.k_empty) + set;
+    const int total = sh.start.left;
+    const int first_head = sh.start.head;
     int head = -1, meetings = 0;
-    for (int n = 0; n < total; n += 2) {
+    Slot<BT> s[2];
+
+    // codes of tile n, of this warp's set
+    auto fetch = [&](Slot<BT> &x, int n) {
+        if (n >= total) {
+            x.head = -1;
+            return true;
+        }
+        const int r = n % META_RING;
+        if (!mbar_wait(&sh.meta_full[r], (n / META_RING) & 1)) return false;
+        pr.fetch(x, sh.meta[r]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
+        return true;
+    };
+    // at every change of heads all producers meet, build the new head's tables and meet again; both
+    // sets pass through every head, with or without a tile in it
+    auto change = [&](int to) {
+        while (head != to) {
+            if (!meet(sh.heads, meetings, lane)) return false;
+            head = head < 0 ? first_head : head + 1;
+            build_table<R>(pr.p, head, table, (set * 4 + sub) * 32 + lane);
+            if (!meet(sh.heads, meetings, lane)) return false;
+        }
+        return true;
+    };
+    if (!fetch(s[0], set)) return false;
+    int use = 0;
+    for (int n = set; n < total; n += 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (n + i >= total) break;
+            if (n + 2 * i >= total) break;
             Slot<BT> &x = s[i];
-            pr.fetch_values(s[1 - i]);
-            if (x.d_head != head) {           // (all producers change heads at the same tile)
-                if (!meet(sh.heads, meetings, lane)) {
-                    sh.failed = 1;
-                    return;
-                }
-                head = x.d_head;
-                build_table<R>(pr.p, head, table, sub * 32 + lane);
-                if (!meet(sh.heads, meetings, lane)) {
-                    sh.failed = 1;
-                    return;
-                }
-            }
-            const int use = (n + i) >> 1;     // times this buffer has been filled
-            if (use > 0 && !mbar_wait(empty + i, (use - 1) & 1)) {
-                sh.failed = 1;
-                return;
-            }
-            pr.decode(x, table, my_tiles + i * TILE_BYTES);
-            if (warp == 0 && lane == 0) sh.mask[(n + i) & (MASK_RING - 1)] = x.mask;
+            if (!fetch(s[1 - i], n + 2 * i + 2)) return false;
+            if (x.head != head && !change(x.head)) return false;
+            if (use > 0 && !mbar_wait(empty, (use - 1) & 1)) return false;
+            ++use;
+            pr.decode(x, table, tile);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full + i);
-            pr.fetch_codes(x);
-            pr.fetch_pages(x, c, first);
+            if (lane == 0) mbar_arrive(full);
         }
     }
+    return change(sh.last_head);
 }
 
 // ---------------------------------------------------------------------------
 // the matrix products: one thread
 // ---------------------------------------------------------------------------
-template <int MT>
-__device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles) {
+template <int MT, int NT>
+__device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles,
+                                               bool leader) {
     constexpr int NB = Shared<MT>::NB;
-    const uint32_t tmem = sh.tmem;
+    using TM = Tmem<MT, NT>;
+    const uint32_t tmem = __shfl_sync(FULL, sh.tmem, 0);
     constexpr uint32_t id_s = mma_idesc(128, PA_TILE, false), id_o = mma_idesc(128, PA_D, true);
     Cursor c = sh.start;
     int tile_no = 0, cnt[MT], pieces[MT];
@@ -476,15 +548,16 @@ __device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT
                     const int no = cnt[g] + i, buf = no % NB, u = no / NB;
                     if (u > 0 && !mbar_wait(&sh.s_empty[g][buf], (u - 1) & 1)) return false;
                     tc_fence_after();
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t b = tiles + st * TILE_BYTES + (k >> 2) * (TILE_BYTES / 2) + (k & 3) * 32;
-                        mma_ts(tmem + Tmem<MT>::s(g, buf), tmem + Tmem<MT>::q(g) + k * 8, smem_desc(b, 16, 1024),
-                               id_s, k > 0);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t b = tiles + st * TILE_BYTES + (k >> 2) * (TILE_BYTES / 2) + (k & 3) * 32;
+                            mma_ts(tmem + TM::s(g, buf), tmem + TM::q(g) + k * 8, smem_desc(b, 16, 1024), id_s, k > 0);
+                        }
+                        mma_commit(&sh.s_full[g][buf]);
                     }
-                    mma_commit(&sh.s_full[g][buf]);
                 }
-                mma_commit(&sh.k_empty[st]);
+                if (leader) mma_commit(&sh.k_empty[st]);
             }
             if (i > 0) {                      // O += P V of tile i - 1
                 const int j = i - 1, st = (tile_no + j) & 1, use = (tile_no + j) >> 1;
@@ -495,16 +568,20 @@ __device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT
                     const int no = cnt[g] + j, buf = no % NB, u = no / NB;
                     if (!mbar_wait(&sh.p_full[g][buf], u & 1)) return false;
                     tc_fence_after();
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t b = tiles + 2 * TILE_BYTES + st * TILE_BYTES + k * 2048;
-                        const uint64_t d = smem_desc(b, TILE_BYTES / 2, 1024);
-                        mma_ts(tmem + Tmem<MT>::o(g), tmem + Tmem<MT>::p(g, buf) + k * 8, d, id_o, j > 0 || k > 0);
-                        mma_ts(tmem + Tmem<MT>::o(g), tmem + Tmem<MT>::p(g, buf) + 16 + k * 8, d, id_o, 1u);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t b = tiles + 2 * TILE_BYTES + st * TILE_BYTES + k * 2048;
+                            const uint64_t d = smem_desc(b, TILE_BYTES / 2, 1024);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                mma_ts(tmem + TM::o(g), tmem + TM::p(g, buf) + 16 * t + 8 * k, d, id_o,
+                                       j > 0 || k > 0 || t > 0);
+                        }
+                        mma_commit(&sh.p_empty[g][buf]);
                     }
-                    mma_commit(&sh.p_empty[g][buf]);
                 }
-                mma_commit(&sh.v_empty[st]);
+                if (leader) mma_commit(&sh.v_empty[st]);
             }
         }
         tile_no += n;
@@ -524,39 +601,74 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// (a0, a1) m + c, and (a0, a1) + (b0, b1), as packed operations.
+__device__ __forceinline__ float2 fma_pair(float a0, float a1, float m, float c) {
+    float2 o;
+    asm("{.reg .b64 t, u, v;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 u, {%4, %4};\n\tmov.b64 v, {%5, %5};\n\t"
+        "fma.rn.f32x2 t, t, u, v;\n\tmov.b64 {%0, %1}, t;}"
+        : "=f"(o.x), "=f"(o.y) : "f"(a0), "f"(a1), "f"(m), "f"(c));
+    return o;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+    float2 o;
+    asm("{.reg .b64 t, u;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 u, {%4, %5};\n\t"
+        "add.rn.f32x2 t, t, u;\n\tmov.b64 {%0, %1}, t;}"
+        : "=f"(o.x), "=f"(o.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return o;
+}
+__device__ __forceinline__ float2 bf16_pair(uint32_t h) {
+    return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+}
 
-// N scores of a row (columns col0 ..), their weights relative to 2^ref as two
-// bf16 terms in p[0 .. N/2) and p[16 .. 16 + N/2); returns their sum.
-template <int N>
-__device__ __forceinline__ float weights(const uint32_t (&s)[N], uint32_t mask, float sl2, float ref,
-                                         uint32_t *hi, uint32_t *lo) {
-    float sum = 0.f;
+// Weights 2^(s sl2 - ref) of N scores as NT bf16 terms (term t of pair j in
+// out[t][j]); sum gets them added.  MASKED: only the columns in mask count.
+template <int N, int NT, bool MASKED>
+__device__ __forceinline__ void weights(const uint32_t *s, uint32_t mask, float sl2, float ref, float2 &sum,
+                                        uint32_t (&out)[NT][N / 2]) {
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-        const float x0 = fmaf(__uint_as_float(s[j]), sl2, -ref), x1 = fmaf(__uint_as_float(s[j + 1]), sl2, -ref);
-        const float p0 = (mask >> j) & 1u ? ex2(x0) : 0.f, p1 = (mask >> (j + 1)) & 1u ? ex2(x1) : 0.f;
-        sum += p0 + p1;
-        const uint32_t h = bf16x2(p0, p1);
-        hi[j / 2] = h;
-        lo[j / 2] = bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u));
+        const float2 x = fma_pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1]), sl2, -ref);
+        float2 p = make_float2(ex2(x.x), ex2(x.y));
+        if (MASKED) {
+            if (!((mask >> j) & 1u)) p.x = 0.f;
+            if (!((mask >> (j + 1)) & 1u)) p.y = 0.f;
+        }
+        sum = add_pair(sum, p);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t h = bf16x2(p.x, p.y);
+            out[t][j / 2] = h;
+            if (t + 1 < NT) {
+                const float2 f = bf16_pair(h);
+                p = add_pair(p, make_float2(-f.x, -f.y));
+            }
+        }
     }
-    return sum;
 }
-template <int N> __device__ __forceinline__ float row_max(const uint32_t (&s)[N], uint32_t mask) {
+template <int N, bool MASKED> __device__ __forceinline__ float row_max(const uint32_t *s, uint32_t mask) {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, (mask >> j) & 1u ? __uint_as_float(s[j]) : -INFINITY);
+    for (int j = 0; j < N; j += 2) {
+        float a = __uint_as_float(s[j]), b = __uint_as_float(s[j + 1]);
+        if (MASKED) {
+            if (!((mask >> j) & 1u)) a = -INFINITY;
+            if (!((mask >> (j + 1)) & 1u)) b = -INFINITY;
+        }
+        m = fmaxf(fmaxf(m, a), b);
+    }
     return m;
 }
 
-template <int MT>
+template <int MT, int NT>
 __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, int warp, int lane) {
     constexpr int NB = Shared<MT>::NB;
+    using TM = Tmem<MT, NT>;
     const int g = warp >> 2, quad = warp & 3;
     const uint32_t tmem = sh.tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t t_o = tmem + Tmem<MT>::o(g), t_q = tmem + Tmem<MT>::q(g);
+    const uint32_t t_o = tmem + TM::o(g), t_q = tmem + TM::q(g);
     Cursor c = sh.start;
     int tile_no = 0, cnt = 0;
+    bool cleared = false;                     // P is zero outside this quarter's columns
     while (c.left > 0) {
         const int n = c.piece();
         const Rows<MT> rows(a, c);
@@ -573,83 +685,95 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             const int gr = rows.base + r;
             const size_t qr = pre ? ((size_t)(gr / a.G) * a.Hk + c.head) * a.G + gr % a.G
                                   : ((size_t)(c.seg - a.row_tiles) * a.Hk + c.head) * a.G + r;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live) v = __ldg(reinterpret_cast<const uint4 *>(a.q + qr * PA_D) + hf * 8 + i);
-                    w[4 * i] = v.x ^ a.q_flip;
-                    w[4 * i + 1] = v.y ^ a.q_flip;
-                    w[4 * i + 2] = v.z ^ a.q_flip;
-                    w[4 * i + 3] = v.w ^ a.q_flip;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qr * PA_D);
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+                uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                if (live) {
+                    v[0] = __ldg(src + 2 * i);
+                    v[1] = __ldg(src + 2 * i + 1);
                 }
-                tmem_st32(t_q + hf * 32, w);
+                const uint32_t f = a.q_flip;
+                const uint32_t w[8] = {v[0].x ^ f, v[0].y ^ f, v[0].z ^ f, v[0].w ^ f,
+                                       v[1].x ^ f, v[1].y ^ f, v[1].z ^ f, v[1].w ^ f};
+                tmem_st8(t_q + 8 * i, w);
             }
+            if (rows.rep && !cleared) {
+                const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 2 * NB * NT; ++i) tmem_st8(tmem + TM::p(g, 0) + 8 * i, z);
+            }
+            cleared = rows.rep;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[g]);
         }
-        float ref = -INFINITY, l = 0.f;       // exponents are relative to ref
+        float ref = -INFINITY;                // exponents are relative to ref
         float m = -INFINITY;                  // largest score so far (times sl2)
+        float2 l = make_float2(0.f, 0.f);
         for (int i = 0; i < n; ++i, ++cnt) {
             const int buf = cnt % NB, u = cnt / NB;
             if (!mbar_wait(&sh.s_full[g][buf], u & 1)) return false;
             tc_fence_after();
-            const uint32_t mask = sh.mask[(tile_no + i) & (MASK_RING - 1)];
-            uint32_t p[32], s[32], s8[8];
+            uint32_t mask = sh.mask[(tile_no + i) % MASK_RING];
+            uint32_t s[32];
             float mt;
             if (rows.rep) {
-                tmem_ld8(tmem + Tmem<MT>::s(g, buf) + 8 * quad, s8);
+                mask = (mask >> (8 * quad)) & 0xFFu;
+                tmem_ld8(tmem + TM::s(g, buf) + 8 * quad, reinterpret_cast<uint32_t(&)[8]>(s));
                 tmem_wait_ld();
-                mt = row_max(s8, mask >> (8 * quad));
+                mt = mask == 0xFFu ? row_max<8, false>(s, mask) : row_max<8, true>(s, mask);
             } else {
-                tmem_ld32(tmem + Tmem<MT>::s(g, buf), s);
+                tmem_ld32(tmem + TM::s(g, buf), s);
                 tmem_wait_ld();
-                mt = row_max(s, mask);
+                mt = mask == 0xFFFFFFFFu ? row_max<32, false>(s, mask) : row_max<32, true>(s, mask);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.s_empty[g][buf]);
             m = fmaxf(m, mt * a.sl2);
             if (__any_sync(FULL, m > ref + PA_RESCALE)) {
-                if (i > 0) {                  // O holds tiles before this one
+                if (i > 0) {                  // O holds the tiles before this one
                     const int pb = (cnt - 1) % NB, pu = (cnt - 1) / NB;
                     if (!mbar_wait(&sh.p_empty[g][pb], pu & 1)) return false;
                     tc_fence_after();
                     const float f = ref == -INFINITY ? 0.f : exp2f(ref - m);
-                    l *= f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + 32 * k, o);
+                    l.x *= f;
+                    l.y *= f;
+#pragma unroll 1
+                    for (int k = 0; k < 16; ++k) {
+                        uint32_t o[8];
+                        tmem_ld8(t_o + 8 * k, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(t_o + 32 * k, o);
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st8(t_o + 8 * k, o);
                     }
                     tmem_wait_st();
                 }
                 ref = m;
             }
             const float rf = ref == -INFINITY ? 0.f : ref;
-            if (rows.rep) {
-                uint32_t h[4], lo[4];
-                l += weights(s8, mask >> (8 * quad), a.sl2, rf, h, lo);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const bool mine = (e >> 2) == quad;
-                    p[e] = mine ? h[e & 3] : 0u;
-                    p[16 + e] = mine ? lo[e & 3] : 0u;
-                }
-            } else {
-                l += weights(s, mask, a.sl2, rf, p, p + 16);
-            }
             if (u > 0 && !mbar_wait(&sh.p_empty[g][buf], (u - 1) & 1)) return false;
             tc_fence_after();
-            tmem_st32(tmem + Tmem<MT>::p(g, buf), p);
+            const uint32_t t_p = tmem + TM::p(g, buf);
+            if (rows.rep) {
+                uint32_t p[NT][4];
+                if (mask == 0xFFu) weights<8, NT, false>(s, mask, a.sl2, rf, l, p);
+                else weights<8, NT, true>(s, mask, a.sl2, rf, l, p);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) tmem_st4(t_p + 16 * t + 4 * quad, p[t]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[NT][8];
+                    if (mask == 0xFFFFFFFFu) weights<16, NT, false>(s + 16 * h, mask, a.sl2, rf, l, p);
+                    else weights<16, NT, true>(s + 16 * h, mask >> (16 * h), a.sl2, rf, l, p);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) tmem_st8(t_p + 16 * t + 8 * h, p[t]);
+                }
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -664,16 +788,15 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
         const int srow = rows.rep ? quad * rows.n + lane : r;
         float *dst = (pre ? a.part_prefix : a.part_own) +
                      (((size_t)seg + blockIdx.x) * slot_rows + srow) * PA_PART;
-        if (live) *reinterpret_cast<float2 *>(dst) = make_float2(ref, l);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            tmem_ld32(t_o + 32 * k, o);
+        if (live) *reinterpret_cast<float2 *>(dst) = make_float2(ref, l.x + l.y);
+#pragma unroll 2
+        for (int k = 0; k < 16; ++k) {
+            uint32_t o[8];
+            tmem_ld8(t_o + 8 * k, o);
             tmem_wait_ld();
             if (live) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(dst + 4 + 32 * k + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<uint4 *>(dst + 4 + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + 8 + 8 * k) = make_uint4(o[4], o[5], o[6], o[7]);
             }
         }
         tc_fence_before();
@@ -683,16 +806,30 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     return true;
 }
 
-template <int BT, int R, int MT>
-__global__ void __launch_bounds__((4 * MT + PROD_WARPS + 1) * 32, 1) k_paged_attn(PagedAttnArgs a) {
-    constexpr int NB = Shared<MT>::NB;
-    extern __shared__ uint8_t dyn[];
-    __shared__ Shared<MT> sh;
+// Warps: 4 MT softmax, 16 producers, the scout, the products and two that
+// only fill the last group of four, which shares registers as a whole: the
+// block is launched with REGS a thread, and each role takes what it needs of
+// their sum.
+template <int MT> struct Roles {
+    static constexpr int SCOUT = 4 * MT + PROD_WARPS;
+    static constexpr int THREADS = (SCOUT + 4) * 32;
+    static constexpr int REGS = MT == 1 ? 80 : 72;
+    static constexpr int SOFTMAX = MT == 1 ? 128 : 80, PRODUCER = 72, REST = MT == 1 ? 64 : 56;
+    static_assert(REGS * THREADS <= 65536, "registers of an SM");
+    static_assert(128 * MT * SOFTMAX + 32 * PROD_WARPS * PRODUCER + 128 * REST <= REGS * THREADS, "register shares");
+};
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <int BT, int R, int MT, int NT>
+__global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __grid_constant__ PagedAttnArgs a) {
+    constexpr int NB = Shared<MT>::NB, SCOUT = Roles<MT>::SCOUT;
+    extern __shared__ __align__(1024) uint8_t dyn[];   // (the swizzle's period)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;         // the swizzle's period
-    const uint32_t tiles = base, tables = base + 4 * TILE_BYTES;
-    if (warp == 4 * MT + PROD_WARPS) {
-        tmem_alloc(&sh.tmem, Tmem<MT>::COLS);
+    const uint32_t tiles = smem_addr(dyn), tables = tiles + 4 * TILE_BYTES;
+    Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + 4 * TILE_BYTES + table_bytes<R>(a.k.S) + table_bytes<R>(a.v.S));
+    if (warp == SCOUT + 1) {
+        tmem_alloc(&sh.tmem, Tmem<MT, NT>::COLS);
         if (lane == 0) {
             sh.failed = 0;
             for (int i = 0; i < 2; ++i) {
@@ -709,6 +846,10 @@ __global__ void __launch_bounds__((4 * MT + PROD_WARPS + 1) * 32, 1) k_paged_att
                     mbar_init(&sh.p_full[g][i], 4);
                     mbar_init(&sh.p_empty[g][i], 1);
                 }
+            }
+            for (int i = 0; i < META_RING; ++i) {
+                mbar_init(&sh.meta_full[i], 1);
+                mbar_init(&sh.meta_empty[i], PROD_WARPS / 2);
             }
             mbar_init(&sh.heads, PROD_WARPS);
             mbar_init(&sh.drain, 1);
@@ -753,26 +894,39 @@ __global__ void __launch_bounds__((4 * MT + PROD_WARPS + 1) * 32, 1) k_paged_att
                 }
             }
         }
-        if (lane == 0) sh.start = c;
+        if (lane == 0) {
+            sh.start = c;
+            sh.last_head = c.left > 0 ? (int)((w.begin(blockIdx.x + 1) - 1) / w.per_head) : 0;
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
+    bool ok = true;
     if (warp < 4 * MT) {
-        if (!softmax<MT>(a, sh, warp, lane)) sh.failed = 1;
-    } else if (warp < 4 * MT + PROD_WARPS) {
-        produce<BT, R, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
-    } else if (lane == 0) {
-        if (!issue_products<MT>(a, sh, tiles)) sh.failed = 1;
-        mma_commit(&sh.drain);                // nothing may be in flight when tensor memory goes
-        if (!mbar_wait(&sh.drain, 0)) sh.failed = 1;
+        regs_up<Roles<MT>::SOFTMAX>();
+        ok = softmax<MT, NT>(a, sh, warp, lane);
+    } else if (warp < SCOUT) {
+        regs_down<Roles<MT>::PRODUCER>();
+        ok = sh.start.left == 0 || produce<BT, R, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
+    } else {
+        regs_down<Roles<MT>::REST>();
+        if (warp == SCOUT) {
+            ok = scout<MT>(a, sh, lane);
+        } else if (warp == SCOUT + 1) {
+            const bool leader = elect_one();
+            ok = issue_products<MT, NT>(a, sh, tiles, leader);
+            if (leader) mma_commit(&sh.drain);    // nothing may be in flight when tensor memory goes
+            if (!mbar_wait(&sh.drain, 0)) ok = false;
+        }
     }
+    if (!ok) sh.failed = 1;
     tc_fence_before();
     __syncthreads();
-    if (warp == 4 * MT + PROD_WARPS) {
+    if (warp == SCOUT + 1) {
         tc_fence_after();
-        tmem_free(sh.tmem, Tmem<MT>::COLS);
+        tmem_free(sh.tmem, Tmem<MT, NT>::COLS);
     }
     if (threadIdx.x == 0 && sh.failed && a.st) atomicOr(&a.st->flags, HQMQ_FLAG_TIMEOUT);
 }
@@ -833,15 +987,17 @@ k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
     if (lse && lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
 }
 
-// Workspace: partials of the prefix's segments, then of the sequences'.
+// Workspace: partials of the prefix's segments, then of the sequences'.  The
+// size covers both output types.
 struct PartPlan {
     int mt, row_tiles, prefix_slot_rows, own_slot_rows;
     uint64_t prefix_bytes, own_bytes;
 };
-inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len) {
+inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len, int out_dtype) {
     PartPlan p;
     const int64_t rows = (int64_t)B * (Hq / Hk);
-    p.mt = prefix_len > 0 && rows > 128 ? 2 : 1;
+    // fp32 outputs take three terms of P, which leaves tensor memory for one group of rows
+    p.mt = prefix_len > 0 && rows > 128 && out_dtype == HQMQ_BF16 ? 2 : 1;
     p.row_tiles = prefix_len > 0 ? (int)((rows + 128 * p.mt - 1) / (128 * p.mt)) : 0;
     p.prefix_slot_rows = rows <= PA_REP_ROWS ? (int)(4 * rows) : 128 * p.mt;
     p.own_slot_rows = 4 * (Hq / Hk);
@@ -850,41 +1006,48 @@ inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len)
     return p;
 }
 
-template <int BT, int R, int MT>
+template <int R, int MT> inline size_t attn_smem_bytes(uint32_t sk, uint32_t sv) {
+    return 4 * TILE_BYTES + table_bytes<R>(sk) + table_bytes<R>(sv) + sizeof(Shared<MT>);
+}
+
+template <int BT, int R, int MT, int NT>
 static int launch_paged_attn(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
                              cudaStream_t stream) {
-    const size_t smem = 1024 + 4 * TILE_BYTES + table_bytes<R>(a.k.S) + table_bytes<R>(a.v.S);
-    auto kern = k_paged_attn<BT, R, MT>;
+    const size_t smem = attn_smem_bytes<R, MT>(a.k.S, a.v.S);
+    auto kern = k_paged_attn<BT, R, MT, NT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
     const int64_t rows = (int64_t)a.B * a.Hk * a.G;
-    if (ctas > 0 && launch_pdl(kern, dim3(ctas), dim3((4 * MT + PROD_WARPS + 1) * 32), smem, stream, a) != cudaSuccess)
+    if (ctas > 0 && launch_pdl(kern, dim3(ctas), dim3(Roles<MT>::THREADS), smem, stream, a) != cudaSuccess)
         return HQMQ_ERR_CUDA;
     return launch_pdl(k_paged_join<MT>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a, o, out_dtype,
                       lse) == cudaSuccess
                ? HQMQ_OK : HQMQ_ERR_CUDA;
 }
 
-template <int MT>
+template <int MT, int NT>
 static int launch_paged_attn_mt(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
                                 cudaStream_t stream) {
     // the index widths of S = 8 and S = 32; 8 table copies (no bank conflicts) where both tables fit
     const bool same = a.k.b == a.v.b;
-    if (same && a.k.b == 8) return launch_paged_attn<8, 8, MT>(a, ctas, o, out_dtype, lse, stream);
-    const bool r8 = 1024 + 4 * TILE_BYTES + table_bytes<8>(a.k.S) + table_bytes<8>(a.v.S) + sizeof(Shared<MT>) <=
-                    227 * 1024;
+    if (same && a.k.b == 8) return launch_paged_attn<8, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
     if (same && a.k.b == 10)
-        return r8 ? launch_paged_attn<10, 8, MT>(a, ctas, o, out_dtype, lse, stream)
-                  : launch_paged_attn<10, 4, MT>(a, ctas, o, out_dtype, lse, stream);
-    return launch_paged_attn<0, 4, MT>(a, ctas, o, out_dtype, lse, stream);
+        return attn_smem_bytes<8, MT>(a.k.S, a.v.S) <= 227 * 1024
+                   ? launch_paged_attn<10, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream)
+                   : launch_paged_attn<10, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+    return launch_paged_attn<0, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
 }
 
 }  // namespace hqmq
 
 extern "C" uint64_t hqmq_paged_attn_workspace_bytes(int B, int Hq, int Hk, int max_tokens,
                                                     int prefix_len) {
-    const hqmq::PartPlan p = hqmq::part_plan(B, Hq, Hk, max_tokens, prefix_len);
-    return ((p.prefix_bytes + p.own_bytes + 255) & ~255ull) + 256;
+    uint64_t n = 0;
+    for (int dt : {HQMQ_BF16, HQMQ_F32}) {
+        const hqmq::PartPlan p = hqmq::part_plan(B, Hq, Hk, max_tokens, prefix_len, dt);
+        if (p.prefix_bytes + p.own_bytes > n) n = p.prefix_bytes + p.own_bytes;
+    }
+    return ((n + 255) & ~255ull) + 256;
 }
 
 extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_pages *k,
@@ -894,7 +1057,7 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
                                            void *o, int out_dtype, float *lse, void *ws,
                                            hqmq_status *st, cudaStream_t stream) {
     using namespace hqmq;
-    const PartPlan p = part_plan(B, Hq, k->heads, max_pages * k->page_size, prefix_len);
+    const PartPlan p = part_plan(B, Hq, k->heads, max_pages * k->page_size, prefix_len, out_dtype);
     PagedAttnArgs a;
     a.q = q;
     a.k = pages_dev(k, bk);
@@ -923,6 +1086,7 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
                                  (int64_t)B * (((int64_t)max_pages * k->page_size + PA_TILE - 1) / PA_TILE));
     const int64_t want = most == 0 ? 0 : most / PA_MIN_TILES < 1 ? 1 : most / PA_MIN_TILES;
     const int ctas = (int)(want < PA_CTAS ? want : PA_CTAS);
-    return p.mt == 2 ? launch_paged_attn_mt<2>(a, ctas, o, out_dtype, lse, stream)
-                     : launch_paged_attn_mt<1>(a, ctas, o, out_dtype, lse, stream);
+    if (out_dtype == HQMQ_F32) return launch_paged_attn_mt<1, 3>(a, ctas, o, out_dtype, lse, stream);
+    return p.mt == 2 ? launch_paged_attn_mt<2, 2>(a, ctas, o, out_dtype, lse, stream)
+                     : launch_paged_attn_mt<1, 2>(a, ctas, o, out_dtype, lse, stream);
 }
