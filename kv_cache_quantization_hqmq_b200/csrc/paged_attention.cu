@@ -4,7 +4,7 @@
 //   o = sum_t softmax_t(scale <q, K^_t>) V^_t
 // over the prefix's tokens and the sequence's own.
 //
-// Work.  Tokens are taken in tiles of 32.  A KV head has these segments: the
+// Work.  Tokens are taken in tiles of 64.  A KV head has these segments: the
 // prefix, once for every 128 MT rows (row = query head of the group of one
 // sequence; all B G of them), then each sequence's own tokens (G rows).  The
 // tiles of all heads form one list, which the CTAs (one per SM) share out
@@ -15,9 +15,12 @@
 //   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // k_paged_attn, warps by role:
-//   * 8 producer warps, 4 for K and 4 for V, decode a tile's codes from
-//     global memory (fetched two tiles ahead, page ids four) through the
-//     head's codeword table in shared memory into bf16 tiles [32 tokens][128]
+//   * one scout warp looks the tiles' pages up (page ids two tiles ahead,
+//     flag words one) and tells the producers where each token's codes and
+//     flagged values lie;
+//   * 16 producer warps, 8 for K and 8 for V, decode a tile's codes from
+//     global memory (fetched a tile ahead) through the head's codeword table
+//     in shared memory into bf16 tiles [64 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
 //   * one warp's elected thread issues the products (tcgen05.mma, 128 rows, accumulators
@@ -28,8 +31,8 @@
 //     maximum has grown by more than 2^8 (then O is rescaled in tensor
 //     memory): weights up to 2^8 lose nothing in floating point.
 // Segments with at most 32 rows put the same rows into each of the four
-// 32-lane quarters; quarter w takes columns 8 w .. 8 w + 7 of every tile (the
-// others get weight 0) and keeps a partial of its own.
+// 32-lane quarters; quarter w takes columns 16 w .. 16 w + 15 of every tile
+// (the others get weight 0) and keeps a partial of its own.
 //
 // Every wait is bounded; one that runs out sets HQMQ_FLAG_TIMEOUT.
 #include "paged.cuh"
@@ -38,15 +41,14 @@
 namespace hqmq {
 
 constexpr int PA_D = 128;
-constexpr int PA_TILE = 32;                   // tokens of a tile
+constexpr int PA_TILE = 64;                   // tokens of a tile
 constexpr int PA_PART = 132;                  // floats of a row's partial: m, l, -, -, O[128]
 constexpr int PA_CTAS = 148;                  // one per SM of a B200
-constexpr int PA_MIN_TILES = 2;               // fewest tiles worth a CTA
 constexpr int PA_REP_ROWS = 32;               // segments up to this many rows are replicated
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
 constexpr int META_RING = 4;                  // tiles
-constexpr int MASK_RING = 16;                 // the scout is at most 12 tiles ahead of the softmax
+constexpr int MASK_RING = 16;                 // the scout is at most 10 tiles ahead of the softmax
 constexpr int PROD_WARPS = 16;
 
 struct PagedAttnArgs {
@@ -97,7 +99,7 @@ struct Shares {
     __device__ __forceinline__ Shares(const PagedAttnArgs &a, int64_t own_total) {
         per_head = (int64_t)a.row_tiles * a.prefix_tiles + own_total;
         total = per_head * a.Hk;
-        ctas = (int)min((int64_t)PA_CTAS, max(total / PA_MIN_TILES, (int64_t)1));
+        ctas = (int)min((int64_t)PA_CTAS, max(total, (int64_t)1));
     }
     __device__ __forceinline__ int64_t begin(int c) const { return c * total / ctas; }
     __device__ __forceinline__ int owner(int64_t tile) const {
@@ -147,38 +149,42 @@ template <int MT> struct Rows {
 
 // What the scout warp finds out about a tile.
 struct Meta {
-    long long page[2];                        // page * heads + head of its halves (16 tokens)
+    long long page[PA_TILE / 16];             // page * heads + head of every 16 tokens
     int row0, head;                           // row of the first token in its page
-    uint32_t mask;                            // valid tokens
-    uint32_t flags[2][PA_TILE];               // flag words of K and V
-    uint16_t start[2][PA_TILE];               // slots of their first values
+    uint32_t mask[2];                         // valid tokens
+    uint2 flags[2][PA_TILE / 2];              // flag words of K and V
+    uint32_t start[2][PA_TILE / 2];           // slots of their first values, 16 bits each
 };
 
 template <int MT> struct Shared {
-    static constexpr int NB = MT == 1 ? 2 : 1;          // S and P buffers of a group
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[MT], s_full[MT][NB], s_empty[MT][NB], p_full[MT][NB], p_empty[MT][NB];
+    uint64_t q_full[MT], s_full[MT][2], s_empty[MT][2], p_full[MT][2], p_empty[MT][2];
     uint64_t meta_full[META_RING], meta_empty[META_RING];
+    uint64_t pair_done;                                 // the second group has left a piece of two groups
     uint64_t heads;                                     // the producers, at a change of heads
     uint64_t drain;
     Meta meta[META_RING];
-    uint32_t mask[MASK_RING];                           // valid tokens of the last tiles
+    uint2 mask[MASK_RING];                              // valid tokens of the last tiles
     Cursor start;
-    int last_head;                                      // of the share
     uint32_t tmem;
     int failed;
 };
 
-// Tensor memory columns: O and Q of every group, then its S and P buffers.
+// Tensor memory columns.  One group of rows: O, Q, two S buffers, two P
+// buffers.  Two groups: O and Q of both, and per group 64 columns X that hold
+// S, and then P in its place; replicated rows, which use one group only, take
+// both X for S and the second group's O for their P buffers.
 template <int MT, int NT> struct Tmem {
-    static constexpr int NB = Shared<MT>::NB;
-    static constexpr uint32_t COLS = 512;
+    static constexpr uint32_t COLS = 512, P_COLS = 32 * NT;
     __device__ __forceinline__ static uint32_t o(int g) { return g * 128; }
     __device__ __forceinline__ static uint32_t q(int g) { return MT * 128 + g * 64; }
-    __device__ __forceinline__ static uint32_t s(int g, int i) { return MT * 192 + (g * NB + i) * 32; }
-    __device__ __forceinline__ static uint32_t p(int g, int i) { return MT * 192 + MT * NB * 32 + (g * NB + i) * 16 * NT; }
-    static_assert(MT * 192 + MT * NB * (32 + 16 * NT) <= 512, "tensor memory");
+    __device__ __forceinline__ static uint32_t s(int i) { return MT * 192 + i * 64; }
+    __device__ __forceinline__ static uint32_t p(int i) { return MT == 1 ? 320 + i * P_COLS : 128 + i * 64; }
+    static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64, "tensor memory");
 };
+// Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P: halves of
+// 32 tokens, each over the columns of its own scores when P replaces S.
+template <int NT> __device__ __forceinline__ uint32_t p_col(int k, int t) { return (k >> 1) * 16 * NT + t * 16 + (k & 1) * 8; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -205,9 +211,9 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------
-// scout: one warp, lane = token of the tile
+// scout: one warp, lane l = tokens 2 l and 2 l + 1 of the tile
 // ---------------------------------------------------------------------------
-// Page ids are fetched four tiles before the tile is handed on, flag words two.
+// Page ids are fetched two tiles before the tile is handed on, flag words one.
 struct Scout {
     const PagedAttnArgs &a;
     const int lane;
@@ -218,9 +224,9 @@ struct Scout {
     uint32_t base;                            // flagged chunks before the next tile in its page, K | V << 16
 
     struct Tile {
-        int head, t0, page;
+        int head, t0, n, page;                // head < 0: none; n tokens
         bool first;
-        uint32_t fk, fv;
+        uint2 fk, fv;
     };
 
     __device__ __forceinline__ Scout(const PagedAttnArgs &a_, const Cursor &c_, int lane_)
@@ -237,9 +243,10 @@ struct Scout {
         if (c.left <= 0) return;
         x.head = c.head;
         x.t0 = c.tile * PA_TILE;
+        x.n = min(len - x.t0, PA_TILE);
         x.first = first;
         x.page = -2;                          // no token
-        if (x.t0 + lane < len) x.page = __ldg(tab + ((x.t0 + lane) >> a.k.page_shift));
+        if (2 * lane < x.n) x.page = __ldg(tab + ((x.t0 + 2 * lane) >> a.k.page_shift));
         --c.left;
         first = ++c.tile >= c.n_tiles;
         if (first) {
@@ -248,19 +255,20 @@ struct Scout {
         }
     }
     __device__ __forceinline__ void flags(Tile &x) {
-        x.fk = x.fv = 0u;
+        x.fk = x.fv = make_uint2(0u, 0u);
         if (x.head < 0) return;
         if (x.page != -2 && (x.page < 0 || x.page >= a.k.n_pages || x.page >= a.v.n_pages)) {
             if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
             x.page = -1;
         }
         if (x.page >= 0) {
-            const size_t at = a.k.at(x.page, x.head, (x.t0 + lane) & (a.k.page_size - 1));
-            if (a.k.flags) x.fk = __ldg(a.k.flags + at);
-            if (a.v.flags) x.fv = __ldg(a.v.flags + at);
+            const size_t at = a.k.at(x.page, x.head, (x.t0 + 2 * lane) & (a.k.page_size - 1));
+            if (a.k.flags) x.fk = __ldg(reinterpret_cast<const uint2 *>(a.k.flags + at));
+            if (a.v.flags) x.fv = __ldg(reinterpret_cast<const uint2 *>(a.v.flags + at));
+            if (2 * lane + 1 >= x.n) x.fk.y = x.fv.y = 0u;
         }
     }
-    __device__ __forceinline__ void hand_on(const Tile &x, Meta &m, uint32_t *mask) {
+    __device__ __forceinline__ void hand_on(const Tile &x, Meta &m, uint2 *mask) {
         const int row0 = x.t0 & (a.k.page_size - 1);
         if (row0 == 0) base = 0;
         else if (x.first) {                   // a piece that starts inside a page
@@ -269,28 +277,35 @@ struct Scout {
             base = pg >= 0 && a.k.flags ? flags_before(a.k.flags + f, row0, lane) : 0u;
             if (pg >= 0 && a.v.flags) base |= flags_before(a.v.flags + f, row0, lane) << 16;
         }
-        const uint32_t n = __popc(x.fk) | (__popc(x.fv) << 16);
+        const uint32_t n0 = __popc(x.fk.x) | (__popc(x.fv.x) << 16);
+        const uint32_t n = n0 + (__popc(x.fk.y) | (__popc(x.fv.y) << 16));
         uint32_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t u = __shfl_up_sync(FULL, inc, o);
             if (lane >= o) inc += u;
         }
-        uint32_t start = base + inc - n;
-        const uint32_t half = __shfl_sync(FULL, inc - n, 16);
-        if (a.k.page_size == 16 && lane >= 16) start -= half;
+        // slots start anew with every page: 8, 16 or more lanes
+        const uint32_t before = __shfl_sync(FULL, inc - n, lane & ~((a.k.page_size >> 1) - 1) & 31);
+        const uint32_t start = base + (inc - n) - before;
         base += __shfl_sync(FULL, inc, 31);
-        const uint32_t ok = __ballot_sync(FULL, x.page >= 0);
         m.flags[0][lane] = x.fk;
         m.flags[1][lane] = x.fv;
-        m.start[0][lane] = (uint16_t)start;
-        m.start[1][lane] = (uint16_t)(start >> 16);
-        if ((lane & 15) == 0) m.page[lane >> 4] = (long long)x.page * a.k.heads + x.head;
+        m.start[0][lane] = (start & 0xFFFFu) | ((start + n0) << 16);
+        m.start[1][lane] = (start >> 16) | ((start + n0) & 0xFFFF0000u);
+        if ((lane & 7) == 0) m.page[lane >> 3] = (long long)x.page * a.k.heads + x.head;
+        const uint32_t ok = __ballot_sync(FULL, x.page >= 0);
+        if (lane < 2) {                       // half of the mask: two groups of 16 tokens
+            const uint32_t g = ok >> (16 * lane);
+            const int rest = x.n - 32 * lane;
+            uint32_t w = ((g & 1u) ? 0xFFFFu : 0u) | ((g & 0x100u) ? 0xFFFF0000u : 0u);
+            if (rest < 32) w &= rest <= 0 ? 0u : (1u << rest) - 1u;
+            m.mask[lane] = w;
+            reinterpret_cast<uint32_t *>(mask)[lane] = w;
+        }
         if (lane == 0) {
             m.row0 = row0;
             m.head = x.head;
-            m.mask = ok;
-            *mask = ok;
         }
     }
 };
@@ -299,18 +314,17 @@ template <int MT>
 __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int lane) {
     Scout s(a, sh.start, lane);
     const int total = sh.start.left;
-    Scout::Tile x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s.pages(x[i]);
+    Scout::Tile x[2];
+    s.pages(x[0]);
+    s.pages(x[1]);
     s.flags(x[0]);
-    s.flags(x[1]);
-    for (int n = 0; n < total; n += 4) {
+    for (int n = 0; n < total; n += 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             if (n + i >= total) break;
-            const int slot = (n + i) % META_RING, use = (n + i) / META_RING;
-            s.flags(x[(i + 2) & 3]);
-            if (use > 0 && !mbar_wait(&sh.meta_empty[slot], (use - 1) & 1)) return false;
+            const int slot = (n + i) % META_RING;
+            s.flags(x[1 - i]);
+            if (!mbar_wait(&sh.meta_empty[slot], (((n + i) / META_RING) & 1) ^ 1)) return false;
             s.hand_on(x[i], sh.meta[slot], &sh.mask[(n + i) % MASK_RING]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_full[slot]);
@@ -328,6 +342,11 @@ __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, in
 // 8 lanes of a 16-byte phase, reading copies lane % R, meet in no bank (R = 8)
 // or in pairs (R = 4).  Entry 24 S is zero, for indices out of range.
 template <int R> __host__ __device__ constexpr uint32_t table_bytes(uint32_t S) { return (24u * S + 1u) * R * 16u; }
+
+// Shared memory: two K and two V tiles, the tables, then Shared.
+template <int RK, int RV> __host__ __device__ constexpr uint32_t attn_table_end(uint32_t sk, uint32_t sv) {
+    return 4u * TILE_BYTES + ((table_bytes<RK>(sk) + table_bytes<RV>(sv) + 127u) & ~127u);
+}
 
 template <int R>
 __device__ __forceinline__ void build_table(const PagesDev &p, int head, uint32_t base, int thread) {
@@ -357,7 +376,7 @@ template <int BT> struct Slot {
     const uint2 *slots;
 };
 
-template <int BT, int R> struct Producer {
+template <int BT> struct Producer {
     const PagesDev &p;
     const int lane, q, tok, which;
 
@@ -370,7 +389,7 @@ template <int BT, int R> struct Producer {
 #pragma unroll
         for (int i = 0; i < RunWords<BT>::N; ++i) s.w[i] = 0u;
         s.f8 = 0u;
-        if (!((m.mask >> tok) & 1u)) return;
+        if (!((m.mask[tok >> 5] >> (tok & 31)) & 1u)) return;
         const long long ph = m.page[tok >> 4];
         const size_t at = ((size_t)ph << p.page_shift) + ((m.row0 + tok) & (p.page_size - 1));
         s.rad = __ldg(reinterpret_cast<const uint4 *>(p.radius + at * PG_CHUNKS) + q);
@@ -379,15 +398,15 @@ template <int BT, int R> struct Producer {
 #pragma unroll
         for (int i = 0; i < RunWords<BT>::N; ++i)
             if (BT || wo + i < b) s.w[i] = __ldg(w + i);
-        const uint32_t f = m.flags[which][tok];
+        const uint32_t f = reinterpret_cast<const uint32_t *>(m.flags[which])[tok];
         s.f8 = (f >> (8 * q)) & 0xFFu;
-        s.slot = m.start[which][tok] + __popc(f & ((1u << (8 * q)) - 1u));
+        s.slot = reinterpret_cast<const uint16_t *>(m.start[which])[tok] + __popc(f & ((1u << (8 * q)) - 1u));
         s.slots = reinterpret_cast<const uint2 *>(p.val) + (size_t)ph * p.cap;
         if (s.f8 && s.slot < p.cap) s.val = __ldg(s.slots + s.slot);
     }
 
     // The lane's 8 chunks to the tile, then the flagged ones over them.
-    __device__ __forceinline__ void decode(const Slot<BT> &s, uint32_t table, uint32_t tile) {
+    template <int R> __device__ __forceinline__ void decode(const Slot<BT> &s, uint32_t table, uint32_t tile) {
         constexpr int N = RunWords<BT>::N, LG = R == 8 ? 7 : 6;
         const uint32_t b = BT ? BT : p.b, sh = (8u * q * b) & 31u;
         uint32_t x[N];
@@ -455,27 +474,24 @@ __device__ __forceinline__ bool meet(uint64_t &bar, int &times, int lane) {
     return mbar_wait(&bar, times++ & 1);
 }
 
-// Warps 0-7 take the even tiles, 8-15 the odd ones; of each eight, four K and
-// four V.  A tile's codes are fetched before the one before it is decoded.
-template <int BT, int R, int MT>
+// Warps 0-7 decode K, 8-15 V, eight tokens each.  A tile's codes are fetched
+// before the one before it is decoded.
+template <int BT, int RK, int RV, int MT>
 __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tables, uint32_t tiles,
                                         int warp, int lane) {
-    const int set = warp >> 3, which = (warp >> 2) & 1, sub = warp & 3;
-    Producer<BT, R> pr(which ? a.v : a.k, which, sub, lane);
-    const uint32_t table = tables + (which ? table_bytes<R>(a.k.S) : 0u);
-    const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u) + set * TILE_BYTES;
-    uint64_t *full = (which ? sh.v_full : sh.k_full) + set, *empty = (which ? sh.v_empty : sh.k_empty) + set;
+    const int which = warp >> 3, sub = warp & 7;
+    const PagesDev &p = which ? a.v : a.k;
+    Producer<BT> pr(p, which, sub, lane);
+    const uint32_t table = tables + (which ? table_bytes<RK>(a.k.S) : 0u);
+    const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u);
+    uint64_t *full = which ? sh.v_full : sh.k_full, *empty = which ? sh.v_empty : sh.k_empty;
     const int total = sh.start.left;
-    const int first_head = sh.start.head;
     int head = -1, meetings = 0;
     Slot<BT> s[2];
 
-    // codes of tile n, of this warp's set
     auto fetch = [&](Slot<BT> &x, int n) {
-        if (n >= total) {
-            x.head = -1;
-            return true;
-        }
+        x.head = -1;
+        if (n >= total) return true;
         const int r = n % META_RING;
         if (!mbar_wait(&sh.meta_full[r], (n / META_RING) & 1)) return false;
         pr.fetch(x, sh.meta[r]);
@@ -483,111 +499,135 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
         if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
         return true;
     };
-    // at every change of heads all producers meet, build the new head's tables and meet again; both
-    // sets pass through every head, with or without a tile in it
-    auto change = [&](int to) {
-        while (head != to) {
-            if (!meet(sh.heads, meetings, lane)) return false;
-            head = head < 0 ? first_head : head + 1;
-            build_table<R>(pr.p, head, table, (set * 4 + sub) * 32 + lane);
-            if (!meet(sh.heads, meetings, lane)) return false;
-        }
-        return true;
-    };
-    if (!fetch(s[0], set)) return false;
-    int use = 0;
-    for (int n = set; n < total; n += 4) {
+    if (!fetch(s[0], 0)) return false;
+    for (int n = 0; n < total; n += 2) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (n + 2 * i >= total) break;
+            if (n + i >= total) break;
             Slot<BT> &x = s[i];
-            if (!fetch(s[1 - i], n + 2 * i + 2)) return false;
-            if (x.head != head && !change(x.head)) return false;
-            if (use > 0 && !mbar_wait(empty, (use - 1) & 1)) return false;
-            ++use;
-            pr.decode(x, table, tile);
+            if (!fetch(s[1 - i], n + i + 1)) return false;
+            if (x.head != head) {             // every producer meets the new head at the same tile
+                if (!meet(sh.heads, meetings, lane)) return false;
+                head = x.head;
+                if (which) build_table<RV>(p, head, table, sub * 32 + lane);
+                else build_table<RK>(p, head, table, sub * 32 + lane);
+                if (!meet(sh.heads, meetings, lane)) return false;
+            }
+            if (!mbar_wait(empty + i, ((n >> 1) & 1) ^ 1)) return false;
+            if (RK == RV || !which) pr.template decode<RK>(x, table, tile + i * TILE_BYTES);
+            else pr.template decode<RV>(x, table, tile + i * TILE_BYTES);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full);
+            if (lane == 0) mbar_arrive(full + i);
         }
     }
-    return change(sh.last_head);
+    return true;
 }
 
 // ---------------------------------------------------------------------------
 // the matrix products: one thread
 // ---------------------------------------------------------------------------
+template <int MT, int NT> struct Products {
+    using TM = Tmem<MT, NT>;
+    Shared<MT> &sh;
+    const uint32_t tmem, tiles;
+    const bool leader;
+
+    // S = Q K^T of the K tile in stage st; arrives on s_full.
+    __device__ __forceinline__ void scores(int g, uint32_t s, int st, uint64_t *done) {
+        constexpr uint32_t idesc = mma_idesc(128, PA_TILE, false);
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_ts(tmem + s, tmem + TM::q(g) + k * 8,
+                       smem_desc(tiles + st * TILE_BYTES + (k >> 2) * (TILE_BYTES / 2) + (k & 3) * 32, 16, 1024), idesc,
+                       k > 0);
+            mma_commit(done);
+        }
+    }
+    // O (+)= P V of the V tile in stage st; arrives on p_empty.
+    __device__ __forceinline__ void output(int g, uint32_t p, int st, bool add, uint64_t *done) {
+        constexpr uint32_t idesc = mma_idesc(128, PA_D, true);
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < PA_TILE / 16; ++k) {
+                const uint64_t d = smem_desc(tiles + (2 + st) * TILE_BYTES + k * 2048, TILE_BYTES / 2, 1024);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma_ts(tmem + TM::o(g), tmem + p + p_col<NT>(k, t), d, idesc, add || k > 0 || t > 0);
+            }
+            mma_commit(done);
+        }
+    }
+};
+
 template <int MT, int NT>
 __device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles,
                                                bool leader) {
-    constexpr int NB = Shared<MT>::NB;
     using TM = Tmem<MT, NT>;
-    const uint32_t tmem = __shfl_sync(FULL, sh.tmem, 0);
-    constexpr uint32_t id_s = mma_idesc(128, PA_TILE, false), id_o = mma_idesc(128, PA_D, true);
+    Products<MT, NT> pr = {sh, __shfl_sync(FULL, sh.tmem, 0), tiles, leader};
     Cursor c = sh.start;
-    int tile_no = 0, cnt[MT], pieces[MT];
+    int no = 0;                               // tiles so far: stage no % 2, phase no / 2
+    uint32_t ph[MT], pq = 0;                  // phases of the groups' two buffers, and of q_full
 #pragma unroll
-    for (int g = 0; g < MT; ++g) cnt[g] = pieces[g] = 0;
+    for (int g = 0; g < MT; ++g) ph[g] = 0;
     while (c.left > 0) {
         const int n = c.piece();
-        const int groups = Rows<MT>(a, c).groups();
+        const Rows<MT> rows(a, c);
+        const int groups = rows.groups();
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
             if (g >= groups) continue;
-            if (!mbar_wait(&sh.q_full[g], pieces[g] & 1)) return false;
-            ++pieces[g];
+            if (!mbar_wait(&sh.q_full[g], (pq >> g) & 1)) return false;
+            pq ^= 1u << g;
         }
-        tc_fence_after();
-        for (int i = 0; i <= n; ++i) {
-            if (i < n) {                      // S = Q K^T of tile i
-                const int st = (tile_no + i) & 1, use = (tile_no + i) >> 1;
-                if (!mbar_wait(&sh.k_full[st], use & 1)) return false;
+        if (MT == 1 || rows.rep) {
+            // S of tile i before P V of tile i - 1: the softmax has two buffers of each
+            uint32_t f = ph[0];
+            for (int i = 0; i <= n; ++i) {
+                if (i < n) {
+                    const int b = i & 1, st = (no + i) & 1;
+                    if (!mbar_wait(&sh.k_full[st], ((no + i) >> 1) & 1)) return false;
+                    if (!mbar_wait(&sh.s_empty[0][b], ((f >> b) & 1) ^ 1)) return false;
+                    pr.scores(0, TM::s(b), st, &sh.s_full[0][b]);
+                    if (leader) mma_commit(&sh.k_empty[st]);
+                }
+                if (i > 0) {
+                    const int j = i - 1, b = j & 1, st = (no + j) & 1;
+                    if (!mbar_wait(&sh.v_full[st], ((no + j) >> 1) & 1)) return false;
+                    if (!mbar_wait(&sh.p_full[0][b], (ph[0] >> b) & 1)) return false;
+                    pr.output(0, TM::p(b), st, j > 0, &sh.p_empty[0][b]);
+                    if (leader) mma_commit(&sh.v_empty[st]);
+                    ph[0] ^= 1u << b;
+                }
+                if (i < n) f ^= 1u << (i & 1);
+            }
+        } else {
+            // P takes the place of S: a group's next scores wait for its P V
+            for (int i = 0; i <= n; ++i) {
+                const int st = (no + i) & 1, sv = (no + i - 1) & 1;
+                if (i < n && !mbar_wait(&sh.k_full[st], ((no + i) >> 1) & 1)) return false;
+                if (i > 0 && !mbar_wait(&sh.v_full[sv], ((no + i - 1) >> 1) & 1)) return false;
 #pragma unroll
                 for (int g = 0; g < MT; ++g) {
                     if (g >= groups) continue;
-                    const int no = cnt[g] + i, buf = no % NB, u = no / NB;
-                    if (u > 0 && !mbar_wait(&sh.s_empty[g][buf], (u - 1) & 1)) return false;
-                    tc_fence_after();
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t b = tiles + st * TILE_BYTES + (k >> 2) * (TILE_BYTES / 2) + (k & 3) * 32;
-                            mma_ts(tmem + TM::s(g, buf), tmem + TM::q(g) + k * 8, smem_desc(b, 16, 1024), id_s, k > 0);
-                        }
-                        mma_commit(&sh.s_full[g][buf]);
+                    if (i > 0) {
+                        if (!mbar_wait(&sh.p_full[g][0], ph[g] & 1)) return false;
+                        pr.output(g, TM::s(g), sv, i > 1, &sh.p_empty[g][0]);
+                        ph[g] ^= 1u;
+                    }
+                    if (i < n) {
+                        if (!mbar_wait(&sh.p_empty[g][0], (ph[g] & 1) ^ 1)) return false;
+                        pr.scores(g, TM::s(g), st, &sh.s_full[g][0]);
                     }
                 }
-                if (leader) mma_commit(&sh.k_empty[st]);
-            }
-            if (i > 0) {                      // O += P V of tile i - 1
-                const int j = i - 1, st = (tile_no + j) & 1, use = (tile_no + j) >> 1;
-                if (!mbar_wait(&sh.v_full[st], use & 1)) return false;
-#pragma unroll
-                for (int g = 0; g < MT; ++g) {
-                    if (g >= groups) continue;
-                    const int no = cnt[g] + j, buf = no % NB, u = no / NB;
-                    if (!mbar_wait(&sh.p_full[g][buf], u & 1)) return false;
-                    tc_fence_after();
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t b = tiles + 2 * TILE_BYTES + st * TILE_BYTES + k * 2048;
-                            const uint64_t d = smem_desc(b, TILE_BYTES / 2, 1024);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                mma_ts(tmem + TM::o(g), tmem + TM::p(g, buf) + 16 * t + 8 * k, d, id_o,
-                                       j > 0 || k > 0 || t > 0);
-                        }
-                        mma_commit(&sh.p_empty[g][buf]);
-                    }
-                }
-                if (leader) mma_commit(&sh.v_empty[st]);
+                if (leader && i > 0) mma_commit(&sh.v_empty[sv]);
+                if (leader && i < n) mma_commit(&sh.k_empty[st]);
             }
         }
-        tile_no += n;
-#pragma unroll
-        for (int g = 0; g < MT; ++g)
-            if (g < groups) cnt[g] += n;
+        no += n;
         c.skip(a, n);
     }
     return true;
@@ -659,29 +699,141 @@ template <int N, bool MASKED> __device__ __forceinline__ float row_max(const uin
     return m;
 }
 
+template <int MT, int NT> struct Softmax {
+    using TM = Tmem<MT, NT>;
+    const PagedAttnArgs &a;
+    Shared<MT> &sh;
+    const int g, quad, lane;
+    const uint32_t lanes;                     // tensor memory address of this warp's lanes
+    float ref, m;                             // exponents are relative to ref; largest score so far (times sl2)
+    float2 l;
+    uint32_t ph;                              // phases of the group's two buffers
+
+    __device__ __forceinline__ void arrive(uint64_t *bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    }
+
+    // Moves ref to m if some row's maximum has outgrown it; `done` completes (phase `par`) with the
+    // products of the tiles before, which O then holds (nullptr: there are none).
+    __device__ __forceinline__ bool rescale(float mt, uint64_t *done, uint32_t par) {
+        m = fmaxf(m, mt * a.sl2);
+        if (!__any_sync(FULL, m > ref + PA_RESCALE)) return true;
+        if (done) {
+            if (!mbar_wait(done, par)) return false;
+            tc_fence_after();
+            const float f = ref == -INFINITY ? 0.f : exp2f(ref - m);
+            l.x *= f;
+            l.y *= f;
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+                uint32_t o[8];
+                tmem_ld8(lanes + TM::o(g) + 8 * k, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(lanes + TM::o(g) + 8 * k, o);
+            }
+            tmem_wait_st();
+        }
+        ref = m;
+        return true;
+    }
+    // The weights of 16 scores to their columns of P.
+    __device__ __forceinline__ void put(const uint32_t *s, uint32_t mask, uint32_t p) {
+        const float rf = ref == -INFINITY ? 0.f : ref;
+        uint32_t w[NT][8];
+        if (mask == 0xFFFFu) weights<16, NT, false>(s, mask, a.sl2, rf, l, w);
+        else weights<16, NT, true>(s, mask, a.sl2, rf, l, w);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tmem_st8(p + 16 * t, w[t]);
+    }
+
+    // Replicated rows: 16 of the tile's columns.
+    __device__ __forceinline__ bool tile_rep(int i, const uint2 &valid) {
+        const int b = i & 1;
+        if (!mbar_wait(&sh.s_full[0][b], (ph >> b) & 1)) return false;
+        tc_fence_after();
+        const uint32_t mask = ((quad & 2 ? valid.y : valid.x) >> (16 * (quad & 1))) & 0xFFFFu;
+        uint32_t s[16];
+        tmem_ld16(lanes + TM::s(b) + 16 * quad, s);
+        tmem_wait_ld();
+        arrive(&sh.s_empty[0][b]);
+        const float mt = mask == 0xFFFFu ? row_max<16, false>(s, mask) : row_max<16, true>(s, mask);
+        if (!rescale(mt, i > 0 ? &sh.p_empty[0][b ^ 1] : nullptr, ((ph >> (b ^ 1)) & 1) ^ 1)) return false;
+        if (!mbar_wait(&sh.p_empty[0][b], ((ph >> b) & 1) ^ 1)) return false;
+        tc_fence_after();
+        put(s, mask, lanes + TM::p(b) + p_col<NT>(quad, 0));
+        tmem_wait_st();
+        arrive(&sh.p_full[0][b]);
+        ph ^= 1u << b;
+        return true;
+    }
+    // A row per thread: all 64 columns; the first half's scores are read again for the weights.
+    __device__ __forceinline__ bool tile_full(int i, const uint2 &valid) {
+        const int b = MT == 1 ? i & 1 : 0;
+        if (!mbar_wait(&sh.s_full[g][b], (ph >> b) & 1)) return false;
+        tc_fence_after();
+        const uint2 mask = valid;
+        const uint32_t ts = lanes + TM::s(MT == 1 ? b : g), tp = MT == 1 ? lanes + TM::p(b) : ts;
+        uint32_t s[32];
+        tmem_ld32(ts, s);
+        tmem_wait_ld();
+        float mt = mask.x == FULL ? row_max<32, false>(s, mask.x) : row_max<32, true>(s, mask.x);
+        tmem_ld32(ts + 32, s);
+        tmem_wait_ld();
+        mt = fmaxf(mt, mask.y == FULL ? row_max<32, false>(s, mask.y) : row_max<32, true>(s, mask.y));
+        // with one buffer the scores were issued after the products before them had ended
+        uint64_t *done = i == 0 ? nullptr : &sh.p_empty[g][MT == 1 ? b ^ 1 : 0];
+        if (!rescale(mt, done, (MT == 1 ? (ph >> (b ^ 1)) & 1 : ph & 1) ^ 1)) return false;
+        if (MT == 1) {
+            if (!mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
+            tc_fence_after();
+        }
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+            if (h == 0) {
+                tmem_ld32(ts, s);
+                tmem_wait_ld();
+                arrive(&sh.s_empty[g][b]);
+            }
+            const uint32_t w = h ? mask.y : mask.x;
+            put(s, w & 0xFFFFu, tp + p_col<NT>(2 * h, 0));
+            put(s + 16, w >> 16, tp + p_col<NT>(2 * h + 1, 0));
+        }
+        tmem_wait_st();
+        arrive(&sh.p_full[g][b]);
+        ph ^= 1u << b;
+        return true;
+    }
+};
+
 template <int MT, int NT>
 __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, int warp, int lane) {
-    constexpr int NB = Shared<MT>::NB;
     using TM = Tmem<MT, NT>;
-    const int g = warp >> 2, quad = warp & 3;
-    const uint32_t tmem = sh.tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t t_o = tmem + TM::o(g), t_q = tmem + TM::q(g);
+    const int quad = warp & 3;
+    Softmax<MT, NT> sm = {a, sh, warp >> 2, quad, lane, sh.tmem + ((uint32_t)(quad * 32) << 16), 0.f, 0.f,
+                          make_float2(0.f, 0.f), 0u};
+    const int g = sm.g;
     Cursor c = sh.start;
-    int tile_no = 0, cnt = 0;
+    int no = 0, pairs = 0;                    // tiles, and pieces of two groups, so far
     bool cleared = false;                     // P is zero outside this quarter's columns
     while (c.left > 0) {
         const int n = c.piece();
         const Rows<MT> rows(a, c);
         if (g >= rows.groups()) {
-            tile_no += n;
+            no += n;
             c.skip(a, n);
             continue;
         }
-        // the rows' queries
         const int r = rows.rep ? lane : g * 128 + quad * 32 + lane;
         const bool live = r < rows.n;
         const bool pre = c.prefix(a);
+        // the rows' queries
         {
+            // (replicated rows keep P where the second group had O)
+            if (MT == 2 && rows.rep && pairs > 0 && !mbar_wait(&sh.pair_done, (pairs - 1) & 1)) return false;
             const int gr = rows.base + r;
             const size_t qr = pre ? ((size_t)(gr / a.G) * a.Hk + c.head) * a.G + gr % a.G
                                   : ((size_t)(c.seg - a.row_tiles) * a.Hk + c.head) * a.G + r;
@@ -696,103 +848,44 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
                 const uint32_t f = a.q_flip;
                 const uint32_t w[8] = {v[0].x ^ f, v[0].y ^ f, v[0].z ^ f, v[0].w ^ f,
                                        v[1].x ^ f, v[1].y ^ f, v[1].z ^ f, v[1].w ^ f};
-                tmem_st8(t_q + 8 * i, w);
+                tmem_st8(sm.lanes + TM::q(g) + 8 * i, w);
             }
             if (rows.rep && !cleared) {
                 const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int i = 0; i < 2 * NB * NT; ++i) tmem_st8(tmem + TM::p(g, 0) + 8 * i, z);
+#pragma unroll 1
+                for (int i = 0; i < (int)TM::P_COLS / 8; ++i) {
+                    tmem_st8(sm.lanes + TM::p(0) + 8 * i, z);
+                    tmem_st8(sm.lanes + TM::p(1) + 8 * i, z);
+                }
             }
             cleared = rows.rep;
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[g]);
+            sm.arrive(&sh.q_full[g]);
         }
-        float ref = -INFINITY;                // exponents are relative to ref
-        float m = -INFINITY;                  // largest score so far (times sl2)
-        float2 l = make_float2(0.f, 0.f);
-        for (int i = 0; i < n; ++i, ++cnt) {
-            const int buf = cnt % NB, u = cnt / NB;
-            if (!mbar_wait(&sh.s_full[g][buf], u & 1)) return false;
-            tc_fence_after();
-            uint32_t mask = sh.mask[(tile_no + i) % MASK_RING];
-            uint32_t s[32];
-            float mt;
-            if (rows.rep) {
-                mask = (mask >> (8 * quad)) & 0xFFu;
-                tmem_ld8(tmem + TM::s(g, buf) + 8 * quad, reinterpret_cast<uint32_t(&)[8]>(s));
-                tmem_wait_ld();
-                mt = mask == 0xFFu ? row_max<8, false>(s, mask) : row_max<8, true>(s, mask);
-            } else {
-                tmem_ld32(tmem + TM::s(g, buf), s);
-                tmem_wait_ld();
-                mt = mask == 0xFFFFFFFFu ? row_max<32, false>(s, mask) : row_max<32, true>(s, mask);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty[g][buf]);
-            m = fmaxf(m, mt * a.sl2);
-            if (__any_sync(FULL, m > ref + PA_RESCALE)) {
-                if (i > 0) {                  // O holds the tiles before this one
-                    const int pb = (cnt - 1) % NB, pu = (cnt - 1) / NB;
-                    if (!mbar_wait(&sh.p_empty[g][pb], pu & 1)) return false;
-                    tc_fence_after();
-                    const float f = ref == -INFINITY ? 0.f : exp2f(ref - m);
-                    l.x *= f;
-                    l.y *= f;
-#pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {
-                        uint32_t o[8];
-                        tmem_ld8(t_o + 8 * k, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st8(t_o + 8 * k, o);
-                    }
-                    tmem_wait_st();
-                }
-                ref = m;
-            }
-            const float rf = ref == -INFINITY ? 0.f : ref;
-            if (u > 0 && !mbar_wait(&sh.p_empty[g][buf], (u - 1) & 1)) return false;
-            tc_fence_after();
-            const uint32_t t_p = tmem + TM::p(g, buf);
-            if (rows.rep) {
-                uint32_t p[NT][4];
-                if (mask == 0xFFu) weights<8, NT, false>(s, mask, a.sl2, rf, l, p);
-                else weights<8, NT, true>(s, mask, a.sl2, rf, l, p);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) tmem_st4(t_p + 16 * t + 4 * quad, p[t]);
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[NT][8];
-                    if (mask == 0xFFFFFFFFu) weights<16, NT, false>(s + 16 * h, mask, a.sl2, rf, l, p);
-                    else weights<16, NT, true>(s + 16 * h, mask >> (16 * h), a.sl2, rf, l, p);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) tmem_st8(t_p + 16 * t + 8 * h, p[t]);
-                }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[g][buf]);
+        sm.ref = sm.m = -INFINITY;
+        sm.l = make_float2(0.f, 0.f);
+        if (rows.rep) {
+            for (int i = 0; i < n; ++i)
+                if (!sm.tile_rep(i, sh.mask[(no + i) % MASK_RING])) return false;
+        } else {
+            for (int i = 0; i < n; ++i)
+                if (!sm.tile_full(i, sh.mask[(no + i) % MASK_RING])) return false;
         }
         // the piece's partial
-        const int pb = (cnt - 1) % NB, pu = (cnt - 1) / NB;
-        if (!mbar_wait(&sh.p_empty[g][pb], pu & 1)) return false;
+        const int lb = MT == 1 || rows.rep ? (n - 1) & 1 : 0;
+        if (!mbar_wait(&sh.p_empty[g][lb], ((sm.ph >> lb) & 1) ^ 1)) return false;
         tc_fence_after();
         const int seg = pre ? c.head * a.row_tiles + c.seg : c.head * a.B + c.seg - a.row_tiles;
         const int slot_rows = pre ? a.prefix_slot_rows : a.own_slot_rows;
         const int srow = rows.rep ? quad * rows.n + lane : r;
         float *dst = (pre ? a.part_prefix : a.part_own) +
                      (((size_t)seg + blockIdx.x) * slot_rows + srow) * PA_PART;
-        if (live) *reinterpret_cast<float2 *>(dst) = make_float2(ref, l.x + l.y);
+        const float l = sm.l.x + sm.l.y;      // (NaN scores alone leave ref at -inf: not "no token")
+        if (live) *reinterpret_cast<float2 *>(dst) = make_float2(sm.ref == -INFINITY && l != 0.f ? 0.f : sm.ref, l);
 #pragma unroll 2
         for (int k = 0; k < 16; ++k) {
             uint32_t o[8];
-            tmem_ld8(t_o + 8 * k, o);
+            tmem_ld8(sm.lanes + TM::o(g) + 8 * k, o);
             tmem_wait_ld();
             if (live) {
                 *reinterpret_cast<uint4 *>(dst + 4 + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -800,7 +893,11 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             }
         }
         tc_fence_before();
-        tile_no += n;
+        if (MT == 2 && rows.groups() == 2) {
+            ++pairs;
+            if (g == 1) sm.arrive(&sh.pair_done);
+        }
+        no += n;
         c.skip(a, n);
     }
     return true;
@@ -821,26 +918,26 @@ template <int MT> struct Roles {
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <int BT, int R, int MT, int NT>
+template <int BT, int RK, int RV, int MT, int NT>
 __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __grid_constant__ PagedAttnArgs a) {
-    constexpr int NB = Shared<MT>::NB, SCOUT = Roles<MT>::SCOUT;
+    constexpr int SCOUT = Roles<MT>::SCOUT;
     extern __shared__ __align__(1024) uint8_t dyn[];   // (the swizzle's period)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tiles = smem_addr(dyn), tables = tiles + 4 * TILE_BYTES;
-    Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + 4 * TILE_BYTES + table_bytes<R>(a.k.S) + table_bytes<R>(a.v.S));
+    Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + attn_table_end<RK, RV>(a.k.S, a.v.S));
     if (warp == SCOUT + 1) {
         tmem_alloc(&sh.tmem, Tmem<MT, NT>::COLS);
         if (lane == 0) {
             sh.failed = 0;
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sh.k_full[i], 4);
-                mbar_init(&sh.v_full[i], 4);
+                mbar_init(&sh.k_full[i], PROD_WARPS / 2);
+                mbar_init(&sh.v_full[i], PROD_WARPS / 2);
                 mbar_init(&sh.k_empty[i], 1);
                 mbar_init(&sh.v_empty[i], 1);
             }
             for (int g = 0; g < MT; ++g) {
                 mbar_init(&sh.q_full[g], 4);
-                for (int i = 0; i < NB; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     mbar_init(&sh.s_full[g][i], 1);
                     mbar_init(&sh.s_empty[g][i], 4);
                     mbar_init(&sh.p_full[g][i], 4);
@@ -849,8 +946,9 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             }
             for (int i = 0; i < META_RING; ++i) {
                 mbar_init(&sh.meta_full[i], 1);
-                mbar_init(&sh.meta_empty[i], PROD_WARPS / 2);
+                mbar_init(&sh.meta_empty[i], PROD_WARPS);
             }
+            mbar_init(&sh.pair_done, 4);
             mbar_init(&sh.heads, PROD_WARPS);
             mbar_init(&sh.drain, 1);
             mbar_init_fence();
@@ -894,10 +992,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
                 }
             }
         }
-        if (lane == 0) {
-            sh.start = c;
-            sh.last_head = c.left > 0 ? (int)((w.begin(blockIdx.x + 1) - 1) / w.per_head) : 0;
-        }
+        if (lane == 0) sh.start = c;
     }
     tc_fence_before();
     __syncthreads();
@@ -909,7 +1004,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         ok = softmax<MT, NT>(a, sh, warp, lane);
     } else if (warp < SCOUT) {
         regs_down<Roles<MT>::PRODUCER>();
-        ok = sh.start.left == 0 || produce<BT, R, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
+        ok = produce<BT, RK, RV, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
     } else {
         regs_down<Roles<MT>::REST>();
         if (warp == SCOUT) {
@@ -1006,15 +1101,15 @@ inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len,
     return p;
 }
 
-template <int R, int MT> inline size_t attn_smem_bytes(uint32_t sk, uint32_t sv) {
-    return 4 * TILE_BYTES + table_bytes<R>(sk) + table_bytes<R>(sv) + sizeof(Shared<MT>);
+template <int RK, int RV, int MT> inline size_t attn_smem_bytes(uint32_t sk, uint32_t sv) {
+    return attn_table_end<RK, RV>(sk, sv) + sizeof(Shared<MT>);
 }
 
-template <int BT, int R, int MT, int NT>
+template <int BT, int RK, int RV, int MT, int NT>
 static int launch_paged_attn(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
                              cudaStream_t stream) {
-    const size_t smem = attn_smem_bytes<R, MT>(a.k.S, a.v.S);
-    auto kern = k_paged_attn<BT, R, MT, NT>;
+    const size_t smem = attn_smem_bytes<RK, RV, MT>(a.k.S, a.v.S);
+    auto kern = k_paged_attn<BT, RK, RV, MT, NT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
     const int64_t rows = (int64_t)a.B * a.Hk * a.G;
@@ -1028,14 +1123,14 @@ static int launch_paged_attn(const PagedAttnArgs &a, int ctas, void *o, int out_
 template <int MT, int NT>
 static int launch_paged_attn_mt(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
                                 cudaStream_t stream) {
-    // the index widths of S = 8 and S = 32; 8 table copies (no bank conflicts) where both tables fit
+    // the index widths of S = 8 and S = 32; 8 table copies (no bank conflicts) where they fit
     const bool same = a.k.b == a.v.b;
-    if (same && a.k.b == 8) return launch_paged_attn<8, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+    if (same && a.k.b == 8) return launch_paged_attn<8, 8, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
     if (same && a.k.b == 10)
-        return attn_smem_bytes<8, MT>(a.k.S, a.v.S) <= 227 * 1024
-                   ? launch_paged_attn<10, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream)
-                   : launch_paged_attn<10, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
-    return launch_paged_attn<0, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+        return attn_smem_bytes<8, 4, MT>(a.k.S, a.v.S) <= 227 * 1024
+                   ? launch_paged_attn<10, 8, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream)
+                   : launch_paged_attn<10, 4, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+    return launch_paged_attn<0, 4, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
 }
 
 }  // namespace hqmq
@@ -1084,8 +1179,7 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
     // tiles there can be at most
     const int64_t most = a.Hk * ((int64_t)a.row_tiles * a.prefix_tiles +
                                  (int64_t)B * (((int64_t)max_pages * k->page_size + PA_TILE - 1) / PA_TILE));
-    const int64_t want = most == 0 ? 0 : most / PA_MIN_TILES < 1 ? 1 : most / PA_MIN_TILES;
-    const int ctas = (int)(want < PA_CTAS ? want : PA_CTAS);
+    const int ctas = (int)(most < PA_CTAS ? most : PA_CTAS);
     if (out_dtype == HQMQ_F32) return launch_paged_attn_mt<1, 3>(a, ctas, o, out_dtype, lse, stream);
     return p.mt == 2 ? launch_paged_attn_mt<2, 2>(a, ctas, o, out_dtype, lse, stream)
                      : launch_paged_attn_mt<1, 2>(a, ctas, o, out_dtype, lse, stream);

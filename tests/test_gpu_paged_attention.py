@@ -198,6 +198,23 @@ def test_nan_values_reach_only_their_rows_and_stale_rows_reach_none():
     assert bool(torch.isnan(out[1][1]).all()) and not bool(torch.isnan(out[0]).any())
 
 
+def test_rows_with_nothing_but_nan_are_nan():
+    """Every score NaN (all radii NaN), in the prefix or in a sequence's own tokens: NaN, not 0."""
+    rng = np.random.default_rng(27)
+    pools = [filled_pool(rng, 4, 1, 16, 8, 0) for _ in range(2)]
+    pools[0]["radius"][1] = 0x7E00
+    (kp, _), (vp, _) = (P.upload(p) for p in pools)
+    for rows in (1, 5):
+        q = torch.from_numpy(rng.standard_normal((rows, 8, 128)).astype(np.float32)).bfloat16().cuda()
+        for prefix, ln in ((16, 0), (0, 16), (16, 16)):
+            for out in (torch.float32, torch.bfloat16):
+                o = torch.zeros(rows, 8, 128, dtype=out, device="cuda")
+                ws = hqmq.alloc_attention_paged_ws(rows, 8, kp, 1, prefix)
+                t_d, l_d, p_d = cuda_ints([[1 if prefix == 0 else 2]] * rows, [ln] * rows, [1])
+                hqmq.hqmq_attention_paged(q, kp, vp, t_d, l_d, o, ws, prefix_table=p_d, prefix_len=prefix)
+                assert bool(torch.isnan(o).all())
+
+
 def test_same_answer_again_on_other_streams_and_in_graphs():
     """Twice the same bits; two captured graphs and an eager call with workspaces of their own, replayed
     together on two streams."""
