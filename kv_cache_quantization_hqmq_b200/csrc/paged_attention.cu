@@ -44,6 +44,7 @@ constexpr int PA_D = 128;
 constexpr int PA_TILE = 64;                   // tokens of a tile
 constexpr int PA_PART = 132;                  // floats of a row's partial: m, l, -, -, O[128]
 constexpr int PA_CTAS = 148;                  // one per SM of a B200
+constexpr int OWN_COST = 2;                   // see prefix_cost
 constexpr int PA_REP_ROWS = 32;               // segments up to this many rows are replicated
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
@@ -54,10 +55,12 @@ constexpr int PROD_WARPS = 16;
 struct PagedAttnArgs {
     const uint16_t *q;
     PagesDev k, v;
+    uint32_t copies_k, copies_v;              // of their codeword tables
     int B, Hk, G, rows;                       // rows = B G of a KV head over the prefix
     const int *seq_len, *table, *prefix_table;
     int max_pages, prefix_len;
     int row_tiles, prefix_tiles;              // segments of the prefix, tiles in each
+    int prefix_cost;                          // of a tile of the prefix; one of a sequence's own costs OWN_COST
     float sl2;                                // |scale| log2(e)
     uint32_t q_flip;                          // sign bits to flip in q (scale < 0)
     float *part_prefix, *part_own;            // [segment + CTA][rows][PA_PART]
@@ -92,41 +95,48 @@ __device__ __forceinline__ int64_t tiles_before(const PagedAttnArgs &a, int b_en
     return before;
 }
 
-// How the list of all heads' tiles is shared out.
+// How the list of all heads' tiles is shared out: by cost, CTA c taking the
+// tiles that start in [c len, (c + 1) len).
 struct Shares {
-    int64_t per_head, total;
-    int ctas;
+    int64_t per_head, total, len;
     __device__ __forceinline__ Shares(const PagedAttnArgs &a, int64_t own_total) {
-        per_head = (int64_t)a.row_tiles * a.prefix_tiles + own_total;
+        per_head = (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost + own_total * OWN_COST;
         total = per_head * a.Hk;
-        ctas = (int)min((int64_t)PA_CTAS, max(total, (int64_t)1));
+        len = total < (1ll << 31) ? (int64_t)(((uint32_t)total + PA_CTAS - 1) / PA_CTAS) : (total + PA_CTAS - 1) / PA_CTAS;
+        // (no less than a tile: the CTAs needed are no more than there are tiles)
+        len = max(len, (int64_t)max(a.prefix_tiles ? a.prefix_cost : 0, OWN_COST));
     }
-    __device__ __forceinline__ int64_t begin(int c) const { return c * total / ctas; }
-    __device__ __forceinline__ int owner(int64_t tile) const {
-        return (int)(((tile + 1) * ctas - 1) / total);
+    __device__ __forceinline__ int owner(int64_t at) const {
+        return at < (1ll << 32) && len < (1ll << 32) ? (int)((uint32_t)at / (uint32_t)len) : (int)(at / len);
     }
 };
 
 // A place in the list: tile `tile` of segment `seg` of `head`.
 struct Cursor {
-    int head, seg, tile, n_tiles, left;       // tiles of the segment, tiles left of the CTA's share
+    int head, seg, tile, n_tiles;             // n_tiles of the segment
+    int64_t left;                             // cost from this tile's start to the end of the CTA's share
+    __device__ __forceinline__ bool prefix(const PagedAttnArgs &a) const { return seg < a.row_tiles; }
+    __device__ __forceinline__ int cost(const PagedAttnArgs &a) const { return prefix(a) ? a.prefix_cost : OWN_COST; }
     __device__ __forceinline__ void settle(const PagedAttnArgs &a) {
         while (left > 0 && tile >= n_tiles) {
             tile = 0;
             if (++seg == a.row_tiles + a.B) {
                 seg = 0;
-                ++head;
+                if (++head == a.Hk) left = 0;
             }
             n_tiles = seg < a.row_tiles ? a.prefix_tiles : own_tiles(a, seg - a.row_tiles);
         }
     }
-    __device__ __forceinline__ int piece() const { return min(n_tiles - tile, left); }
+    __device__ __forceinline__ int piece(const PagedAttnArgs &a) const {
+        const int c = cost(a);
+        const int64_t most = (left + c - 1) / c;
+        return most < n_tiles - tile ? (int)most : n_tiles - tile;
+    }
     __device__ __forceinline__ void skip(const PagedAttnArgs &a, int n) {
+        left -= (int64_t)n * cost(a);
         tile += n;
-        left -= n;
         settle(a);
     }
-    __device__ __forceinline__ bool prefix(const PagedAttnArgs &a) const { return seg < a.row_tiles; }
 };
 
 // Rows of a segment, whether they are replicated, and its softmax groups.
@@ -166,6 +176,7 @@ template <int MT> struct Shared {
     Meta meta[META_RING];
     uint2 mask[MASK_RING];                              // valid tokens of the last tiles
     Cursor start;
+    int total;                                          // tiles of the share
     uint32_t tmem;
     int failed;
 };
@@ -247,7 +258,7 @@ struct Scout {
         x.first = first;
         x.page = -2;                          // no token
         if (2 * lane < x.n) x.page = __ldg(tab + ((x.t0 + 2 * lane) >> a.k.page_shift));
-        --c.left;
+        c.left -= c.cost(a);
         first = ++c.tile >= c.n_tiles;
         if (first) {
             c.settle(a);
@@ -313,7 +324,7 @@ struct Scout {
 template <int MT>
 __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int lane) {
     Scout s(a, sh.start, lane);
-    const int total = sh.start.left;
+    const int total = sh.total;
     Scout::Tile x[2];
     s.pages(x[0]);
     s.pages(x[1]);
@@ -341,21 +352,19 @@ __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, in
 // Codeword table of a head: entry i, copy r at byte (i R + r) 16, so that the
 // 8 lanes of a 16-byte phase, reading copies lane % R, meet in no bank (R = 8)
 // or in pairs (R = 4).  Entry 24 S is zero, for indices out of range.
-template <int R> __host__ __device__ constexpr uint32_t table_bytes(uint32_t S) { return (24u * S + 1u) * R * 16u; }
-
+__host__ __device__ constexpr uint32_t table_bytes(uint32_t S, uint32_t R) { return (24u * S + 1u) * R * 16u; }
 // Shared memory: two K and two V tiles, the tables, then Shared.
-template <int RK, int RV> __host__ __device__ constexpr uint32_t attn_table_end(uint32_t sk, uint32_t sv) {
-    return 4u * TILE_BYTES + ((table_bytes<RK>(sk) + table_bytes<RV>(sv) + 127u) & ~127u);
+__host__ __device__ constexpr uint32_t attn_table_end(uint32_t sk, uint32_t rk, uint32_t sv, uint32_t rv) {
+    return 4u * TILE_BYTES + ((table_bytes(sk, rk) + table_bytes(sv, rv) + 127u) & ~127u);
 }
 
-template <int R>
-__device__ __forceinline__ void build_table(const PagesDev &p, int head, uint32_t base, int thread) {
+__device__ __forceinline__ void build_table(const PagesDev &p, uint32_t R, int head, uint32_t base, int thread) {
     const uint32_t n = 24u * p.S;
     for (uint32_t e = thread; e <= n; e += PROD_WARPS * 16) {
         float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
         if (e < n) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+#pragma unroll 1
+        for (uint32_t r = 0; r < R; ++r)
             sts128(base + (e * R + ((r + e) & (R - 1))) * 16, __float_as_uint(c.x), __float_as_uint(c.y),
                    __float_as_uint(c.z), __float_as_uint(c.w));
     }
@@ -379,9 +388,11 @@ template <int BT> struct Slot {
 template <int BT> struct Producer {
     const PagesDev &p;
     const int lane, q, tok, which;
+    const uint32_t stride, copy;              // bytes of a table entry, this lane's copy in the table
 
-    __device__ __forceinline__ Producer(const PagesDev &p_, int which_, int sub, int lane_)
-        : p(p_), lane(lane_), q(lane_ >> 3), tok(sub * 8 + (lane_ & 7)), which(which_) {}
+    __device__ __forceinline__ Producer(const PagesDev &p_, int which_, int sub, int lane_, uint32_t R, uint32_t table)
+        : p(p_), lane(lane_), q(lane_ >> 3), tok(sub * 8 + (lane_ & 7)), which(which_), stride(R * 16u),
+          copy(table + (lane_ & (R - 1u)) * 16u) {}
 
     __device__ __forceinline__ void fetch(Slot<BT> &s, const Meta &m) {
         s.head = m.head;
@@ -406,15 +417,14 @@ template <int BT> struct Producer {
     }
 
     // The lane's 8 chunks to the tile, then the flagged ones over them.
-    template <int R> __device__ __forceinline__ void decode(const Slot<BT> &s, uint32_t table, uint32_t tile) {
-        constexpr int N = RunWords<BT>::N, LG = R == 8 ? 7 : 6;
+    __device__ __forceinline__ void decode(const Slot<BT> &s, uint32_t tile) {
+        constexpr int N = RunWords<BT>::N;
         const uint32_t b = BT ? BT : p.b, sh = (8u * q * b) & 31u;
         uint32_t x[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
             x[i] = BT == 8 ? s.w[i] : i + 1 < N ? __funnelshift_r(s.w[i], s.w[i + 1], sh) : s.w[i] >> sh;
-        const uint32_t copy = (uint32_t)(lane & (R - 1)) * 16u;
-        const uint32_t zero = ((24u * p.S) << LG) | copy;
+        const uint32_t zero = 24u * p.S;
         const uint32_t row = tile + (q >> 1) * (TILE_BYTES / 2) + (tok >> 3) * 1024 + (tok & 7) * 128;
         const uint32_t u0 = (q & 1) * 4, swz = tok & 7;
 #pragma unroll
@@ -423,12 +433,12 @@ template <int BT> struct Producer {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int j = 4 * h + k;
-                uint32_t v;                   // index << LG, other bits around it
+                uint32_t v;                   // the index, other bits above it
                 if (BT) {
                     constexpr int BB = BT ? BT : 1;
                     const int pos = j * BB, wi = pos >> 5, s5 = pos & 31;
-                    if (s5 + BB > 32 && wi + 1 < N) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5 - LG);
-                    else v = s5 >= LG ? x[wi] >> (s5 - LG) : x[wi] << (LG - s5);
+                    if (s5 + BB > 32 && wi + 1 < N) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5);
+                    else v = x[wi] >> s5;
                 } else {
                     const uint32_t pos = j * b, wi = pos >> 5, s5 = pos & 31u;
                     uint32_t lo = x[0], hi = x[1];
@@ -438,9 +448,9 @@ template <int BT> struct Producer {
                             lo = x[i];
                             hi = i + 1 < N ? x[i + 1] : 0u;
                         }
-                    v = __funnelshift_r(lo, hi, s5) << LG;
+                    v = __funnelshift_r(lo, hi, s5);
                 }
-                c[k] = lds128(table + min((v & (((1u << b) - 1u) << LG)) | copy, zero));
+                c[k] = lds128(min(v & ((1u << b) - 1u), zero) * stride + copy);
             }
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
@@ -476,50 +486,44 @@ __device__ __forceinline__ bool meet(uint64_t &bar, int &times, int lane) {
 
 // Warps 0-7 decode K, 8-15 V, eight tokens each.  A tile's codes are fetched
 // before the one before it is decoded.
-template <int BT, int RK, int RV, int MT>
+template <int BT, int MT>
 __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tables, uint32_t tiles,
                                         int warp, int lane) {
     const int which = warp >> 3, sub = warp & 7;
     const PagesDev &p = which ? a.v : a.k;
-    Producer<BT> pr(p, which, sub, lane);
-    const uint32_t table = tables + (which ? table_bytes<RK>(a.k.S) : 0u);
+    const uint32_t R = which ? a.copies_v : a.copies_k;
+    const uint32_t table = tables + (which ? table_bytes(a.k.S, a.copies_k) : 0u);
+    Producer<BT> pr(p, which, sub, lane, R, table);
     const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u);
     uint64_t *full = which ? sh.v_full : sh.k_full, *empty = which ? sh.v_empty : sh.k_empty;
-    const int total = sh.start.left;
+    const int total = sh.total;
     int head = -1, meetings = 0;
-    Slot<BT> s[2];
+    Slot<BT> x, next;
 
-    auto fetch = [&](Slot<BT> &x, int n) {
-        x.head = -1;
-        if (n >= total) return true;
-        const int r = n % META_RING;
-        if (!mbar_wait(&sh.meta_full[r], (n / META_RING) & 1)) return false;
-        pr.fetch(x, sh.meta[r]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
-        return true;
-    };
-    if (!fetch(s[0], 0)) return false;
-    for (int n = 0; n < total; n += 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (n + i >= total) break;
-            Slot<BT> &x = s[i];
-            if (!fetch(s[1 - i], n + i + 1)) return false;
-            if (x.head != head) {             // every producer meets the new head at the same tile
-                if (!meet(sh.heads, meetings, lane)) return false;
-                head = x.head;
-                if (which) build_table<RV>(p, head, table, sub * 32 + lane);
-                else build_table<RK>(p, head, table, sub * 32 + lane);
-                if (!meet(sh.heads, meetings, lane)) return false;
-            }
-            if (!mbar_wait(empty + i, ((n >> 1) & 1) ^ 1)) return false;
-            if (RK == RV || !which) pr.template decode<RK>(x, table, tile + i * TILE_BYTES);
-            else pr.template decode<RV>(x, table, tile + i * TILE_BYTES);
-            fence_async_smem();
+    next.head = -1;
+#pragma unroll 1
+    for (int n = -1; n < total; ++n) {
+        x = next;
+        if (n + 1 < total) {
+            const int r = (n + 1) % META_RING;
+            if (!mbar_wait(&sh.meta_full[r], ((n + 1) / META_RING) & 1)) return false;
+            pr.fetch(next, sh.meta[r]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(full + i);
+            if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
         }
+        if (n < 0) continue;
+        if (x.head != head) {                 // every producer meets the new head at the same tile
+            if (!meet(sh.heads, meetings, lane)) return false;
+            head = x.head;
+            build_table(p, R, head, table, sub * 32 + lane);
+            if (!meet(sh.heads, meetings, lane)) return false;
+        }
+        const int st = n & 1;
+        if (!mbar_wait(empty + st, ((n >> 1) & 1) ^ 1)) return false;
+        pr.decode(x, tile + st * TILE_BYTES);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + st);
     }
     return true;
 }
@@ -574,7 +578,7 @@ __device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT
 #pragma unroll
     for (int g = 0; g < MT; ++g) ph[g] = 0;
     while (c.left > 0) {
-        const int n = c.piece();
+        const int n = c.piece(a);
         const Rows<MT> rows(a, c);
         const int groups = rows.groups();
 #pragma unroll
@@ -660,19 +664,14 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t h) {
     return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
 }
 
-// Weights 2^(s sl2 - ref) of N scores as NT bf16 terms (term t of pair j in
-// out[t][j]); sum gets them added.  MASKED: only the columns in mask count.
-template <int N, int NT, bool MASKED>
-__device__ __forceinline__ void weights(const uint32_t *s, uint32_t mask, float sl2, float ref, float2 &sum,
-                                        uint32_t (&out)[NT][N / 2]) {
+// Weights 2^(s sl2 - ref) of 16 scores as NT bf16 terms (term t of pair j in
+// out[t][j]); sum gets them added.
+template <int NT>
+__device__ __forceinline__ void weights(const uint32_t *s, float sl2, float ref, float2 &sum, uint32_t (&out)[NT][8]) {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
+    for (int j = 0; j < 16; j += 2) {
         const float2 x = fma_pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1]), sl2, -ref);
         float2 p = make_float2(ex2(x.x), ex2(x.y));
-        if (MASKED) {
-            if (!((mask >> j) & 1u)) p.x = 0.f;
-            if (!((mask >> (j + 1)) & 1u)) p.y = 0.f;
-        }
         sum = add_pair(sum, p);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -685,18 +684,20 @@ __device__ __forceinline__ void weights(const uint32_t *s, uint32_t mask, float 
         }
     }
 }
-template <int N, bool MASKED> __device__ __forceinline__ float row_max(const uint32_t *s, uint32_t mask) {
-    float m = -INFINITY;
+template <int N> __device__ __forceinline__ float row_max(const uint32_t *s) {
+    float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        float a = __uint_as_float(s[j]), b = __uint_as_float(s[j + 1]);
-        if (MASKED) {
-            if (!((mask >> j) & 1u)) a = -INFINITY;
-            if (!((mask >> (j + 1)) & 1u)) b = -INFINITY;
-        }
-        m = fmaxf(fmaxf(m, a), b);
+    for (int j = 0; j < N; j += 4) {
+        m0 = fmaxf(fmaxf(m0, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+        m1 = fmaxf(fmaxf(m1, __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
     }
-    return m;
+    return fmaxf(m0, m1);
+}
+// Scores of columns that are not in the mask become -inf (weight 0: sl2 > 0).
+template <int N> __device__ __forceinline__ void hide(uint32_t (&s)[N], uint32_t mask) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (!((mask >> j) & 1u)) s[j] = 0xFF800000u;
 }
 
 template <int MT, int NT> struct Softmax {
@@ -741,11 +742,9 @@ template <int MT, int NT> struct Softmax {
         return true;
     }
     // The weights of 16 scores to their columns of P.
-    __device__ __forceinline__ void put(const uint32_t *s, uint32_t mask, uint32_t p) {
-        const float rf = ref == -INFINITY ? 0.f : ref;
+    __device__ __forceinline__ void put(const uint32_t *s, float rf, uint32_t p) {
         uint32_t w[NT][8];
-        if (mask == 0xFFFFu) weights<16, NT, false>(s, mask, a.sl2, rf, l, w);
-        else weights<16, NT, true>(s, mask, a.sl2, rf, l, w);
+        weights<NT>(s, a.sl2, rf, l, w);
 #pragma unroll
         for (int t = 0; t < NT; ++t) tmem_st8(p + 16 * t, w[t]);
     }
@@ -760,30 +759,33 @@ template <int MT, int NT> struct Softmax {
         tmem_ld16(lanes + TM::s(b) + 16 * quad, s);
         tmem_wait_ld();
         arrive(&sh.s_empty[0][b]);
-        const float mt = mask == 0xFFFFu ? row_max<16, false>(s, mask) : row_max<16, true>(s, mask);
-        if (!rescale(mt, i > 0 ? &sh.p_empty[0][b ^ 1] : nullptr, ((ph >> (b ^ 1)) & 1) ^ 1)) return false;
+        if (mask != 0xFFFFu) hide(s, mask);
+        if (!rescale(row_max<16>(s), i > 0 ? &sh.p_empty[0][b ^ 1] : nullptr, ((ph >> (b ^ 1)) & 1) ^ 1)) return false;
         if (!mbar_wait(&sh.p_empty[0][b], ((ph >> b) & 1) ^ 1)) return false;
         tc_fence_after();
-        put(s, mask, lanes + TM::p(b) + p_col<NT>(quad, 0));
+        put(s, ref == -INFINITY ? 0.f : ref, lanes + TM::p(b) + p_col<NT>(quad, 0));
         tmem_wait_st();
         arrive(&sh.p_full[0][b]);
         ph ^= 1u << b;
         return true;
     }
-    // A row per thread: all 64 columns; the first half's scores are read again for the weights.
+    // A row per thread: all 64 columns, in halves, read once for the maximum and again for the weights.
     __device__ __forceinline__ bool tile_full(int i, const uint2 &valid) {
         const int b = MT == 1 ? i & 1 : 0;
         if (!mbar_wait(&sh.s_full[g][b], (ph >> b) & 1)) return false;
         tc_fence_after();
         const uint2 mask = valid;
         const uint32_t ts = lanes + TM::s(MT == 1 ? b : g), tp = MT == 1 ? lanes + TM::p(b) : ts;
+        float mt = -INFINITY;
         uint32_t s[32];
-        tmem_ld32(ts, s);
-        tmem_wait_ld();
-        float mt = mask.x == FULL ? row_max<32, false>(s, mask.x) : row_max<32, true>(s, mask.x);
-        tmem_ld32(ts + 32, s);
-        tmem_wait_ld();
-        mt = fmaxf(mt, mask.y == FULL ? row_max<32, false>(s, mask.y) : row_max<32, true>(s, mask.y));
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            tmem_ld32(ts + 32 * h, s);
+            tmem_wait_ld();
+            const uint32_t w = h ? mask.y : mask.x;
+            if (w != FULL) hide(s, w);
+            mt = fmaxf(mt, row_max<32>(s));
+        }
         // with one buffer the scores were issued after the products before them had ended
         uint64_t *done = i == 0 ? nullptr : &sh.p_empty[g][MT == 1 ? b ^ 1 : 0];
         if (!rescale(mt, done, (MT == 1 ? (ph >> (b ^ 1)) & 1 : ph & 1) ^ 1)) return false;
@@ -791,18 +793,19 @@ template <int MT, int NT> struct Softmax {
             if (!mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
             tc_fence_after();
         }
-#pragma unroll
-        for (int h = 1; h >= 0; --h) {
-            if (h == 0) {
-                tmem_ld32(ts, s);
-                tmem_wait_ld();
-                arrive(&sh.s_empty[g][b]);
-            }
+        const float rf = ref == -INFINITY ? 0.f : ref;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            tmem_ld32(ts + 32 * h, s);
+            tmem_wait_ld();
+            if (MT == 1 && h == 1) arrive(&sh.s_empty[g][b]);
             const uint32_t w = h ? mask.y : mask.x;
-            put(s, w & 0xFFFFu, tp + p_col<NT>(2 * h, 0));
-            put(s + 16, w >> 16, tp + p_col<NT>(2 * h + 1, 0));
+            if (w != FULL) hide(s, w);
+            put(s, rf, tp + p_col<NT>(2 * h, 0));
+            put(s + 16, rf, tp + p_col<NT>(2 * h + 1, 0));
         }
         tmem_wait_st();
+        if (MT == 2) arrive(&sh.s_empty[g][b]);
         arrive(&sh.p_full[g][b]);
         ph ^= 1u << b;
         return true;
@@ -820,7 +823,7 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     int no = 0, pairs = 0;                    // tiles, and pieces of two groups, so far
     bool cleared = false;                     // P is zero outside this quarter's columns
     while (c.left > 0) {
-        const int n = c.piece();
+        const int n = c.piece(a);
         const Rows<MT> rows(a, c);
         if (g >= rows.groups()) {
             no += n;
@@ -918,13 +921,13 @@ template <int MT> struct Roles {
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <int BT, int RK, int RV, int MT, int NT>
+template <int BT, int MT, int NT>
 __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __grid_constant__ PagedAttnArgs a) {
     constexpr int SCOUT = Roles<MT>::SCOUT;
     extern __shared__ __align__(1024) uint8_t dyn[];   // (the swizzle's period)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tiles = smem_addr(dyn), tables = tiles + 4 * TILE_BYTES;
-    Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + attn_table_end<RK, RV>(a.k.S, a.v.S));
+    Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + attn_table_end(a.k.S, a.copies_k, a.v.S, a.copies_v));
     if (warp == SCOUT + 1) {
         tmem_alloc(&sh.tmem, Tmem<MT, NT>::COLS);
         if (lane == 0) {
@@ -960,21 +963,23 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         tiles_before(a, 0, &own_total);
         const Shares w(a, own_total);
         Cursor c = {0, 0, 0, 0, 0};
-        if (w.total > 0 && (int)blockIdx.x < w.ctas) {
-            const int64_t t0 = w.begin(blockIdx.x);
-            c.left = (int)(w.begin(blockIdx.x + 1) - t0);
-            c.head = (int)(t0 / w.per_head);
-            int64_t rem = t0 - c.head * w.per_head;
-            const int64_t pre = (int64_t)a.row_tiles * a.prefix_tiles;
+        const int64_t from = blockIdx.x * w.len;
+        if (from < w.total) {
+            c.left = min(w.len, w.total - from);
+            c.head = (int)(from / w.per_head);
+            int64_t rem = from - c.head * w.per_head;
+            const int64_t pre = (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost;
+            int64_t at = 0;                   // cost from the segment's start
             if (rem < pre) {
-                c.seg = (int)(rem / a.prefix_tiles);
-                c.tile = (int)(rem % a.prefix_tiles);
+                const int64_t seg = (int64_t)a.prefix_tiles * a.prefix_cost;
+                c.seg = (int)(rem / seg);
                 c.n_tiles = a.prefix_tiles;
+                at = rem - c.seg * seg;
             } else {
                 rem -= pre;
                 for (int b0 = 0; b0 < a.B; b0 += 32) {
                     const int n = b0 + lane < a.B ? own_tiles(a, b0 + lane) : 0;
-                    int64_t inc = n;
+                    int64_t inc = (int64_t)n * OWN_COST;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int64_t u = __shfl_up_sync(FULL, inc, o);
@@ -985,13 +990,25 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
                         const int src = __ffs(hit) - 1;
                         c.seg = a.row_tiles + b0 + src;
                         c.n_tiles = __shfl_sync(FULL, n, src);
-                        c.tile = (int)(rem - __shfl_sync(FULL, inc - n, src));
+                        at = rem - __shfl_sync(FULL, inc - (int64_t)n * OWN_COST, src);
                         break;
                     }
                     rem -= __shfl_sync(FULL, inc, 31);
                 }
             }
+            // the first tile that starts in the share
+            const int cost = c.cost(a);
+            c.tile = (int)((at + cost - 1) / cost);
+            c.left -= (int64_t)c.tile * cost - at;
+            c.settle(a);
         }
+        int total = 0;                        // tiles of the share
+        for (Cursor d = c; d.left > 0;) {
+            const int n = d.piece(a);
+            total += n;
+            d.skip(a, n);
+        }
+        if (lane == 0) sh.total = total;
         if (lane == 0) sh.start = c;
     }
     tc_fence_before();
@@ -1004,7 +1021,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         ok = softmax<MT, NT>(a, sh, warp, lane);
     } else if (warp < SCOUT) {
         regs_down<Roles<MT>::PRODUCER>();
-        ok = produce<BT, RK, RV, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
+        ok = produce<BT, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
     } else {
         regs_down<Roles<MT>::REST>();
         if (warp == SCOUT) {
@@ -1038,39 +1055,63 @@ k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
     int64_t own_total;
     const int64_t before = tiles_before(a, b, &own_total);
     const Shares w(a, own_total);
+    // where the row's partials are: those of the prefix, then those of its own tokens
+    int n_pre = 0, n_own = 0, copies = 1, stride = 0;
+    const float *pre = nullptr, *own = nullptr;
+    size_t pre_step = 0, own_step = 0;        // from one CTA's slot to the next
+    const int64_t head0 = head * w.per_head;
+    if (a.prefix_tiles) {
+        const int r = b * a.G + g, rt = r / (128 * MT);
+        const bool rep = a.rows <= PA_REP_ROWS;
+        const int64_t at = head0 + (int64_t)rt * a.prefix_tiles * a.prefix_cost;
+        const int c0 = w.owner(at), c1 = w.owner(at + (int64_t)(a.prefix_tiles - 1) * a.prefix_cost);
+        copies = rep ? 4 : 1;
+        stride = a.rows * PA_PART;
+        n_pre = (c1 - c0 + 1) * copies;
+        pre_step = (size_t)a.prefix_slot_rows * PA_PART;
+        pre = a.part_prefix + ((size_t)head * a.row_tiles + rt + c0) * pre_step + (rep ? r : r % (128 * MT)) * PA_PART;
+    }
+    if (const int n = own_tiles(a, b)) {
+        const int64_t at = head0 + (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost + before * OWN_COST;
+        const int c0 = w.owner(at), c1 = w.owner(at + (int64_t)(n - 1) * OWN_COST);
+        n_own = (c1 - c0 + 1) * 4;
+        own_step = (size_t)a.own_slot_rows * PA_PART;
+        own = a.part_own + ((size_t)head * a.B + b + c0) * own_step + g * PA_PART;
+    }
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the partials of one segment: `copies` rows `stride` apart in each slot
-    auto take = [&](int64_t first_tile, int n_tiles, const float *part, int64_t seg, int slot_rows, int srow,
-                    int copies, int stride) {
-        if (n_tiles == 0) return;
-        const int c1 = w.owner(first_tile + n_tiles - 1);
-        for (int c = w.owner(first_tile); c <= c1; ++c) {
-            for (int k = 0; k < copies; ++k) {
-                const float *p = part + ((seg + c) * slot_rows + srow + k * stride) * PA_PART;
-                const float2 ml = *reinterpret_cast<const float2 *>(p);
-                const float4 v = *reinterpret_cast<const float4 *>(p + 4 + 4 * lane);
-                if (ml.x == -INFINITY) continue;             // no token
-                const float mn = fmaxf(m, ml.x);
-                const float f0 = exp2f(m - mn), f1 = exp2f(ml.x - mn);
-                m = mn;
-                l = l * f0 + ml.y * f1;
-                acc.x = acc.x * f0 + v.x * f1;
-                acc.y = acc.y * f0 + v.y * f1;
-                acc.z = acc.z * f0 + v.z * f1;
-                acc.w = acc.w * f0 + v.w * f1;
-            }
+    for (int i0 = 0; i0 < n_pre + n_own; i0 += 32) {       // a lane looks at one partial
+        const int i = i0 + lane, j = i - n_pre, n = min(32, n_pre + n_own - i0);
+        const float *p = nullptr;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (i < n_pre) p = pre + (size_t)(copies == 4 ? i >> 2 : i) * pre_step + (copies == 4 ? (i & 3) * stride : 0);
+        else if (j < n_own) p = own + (size_t)(j >> 2) * own_step + (j & 3) * a.G * PA_PART;
+        if (p) ml = *reinterpret_cast<const float2 *>(p);
+        float mn = ml.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, o));
+        mn = fmaxf(mn, m);
+        const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);         // (-inf: no token)
+        float sum = ml.x == -INFINITY ? 0.f : ml.y * f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        m = mn;
+        l = l * f0 + sum;
+        acc.x *= f0; acc.y *= f0; acc.z *= f0; acc.w *= f0;
+        const unsigned there = __ballot_sync(FULL, ml.x != -INFINITY && p != nullptr);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(FULL, f, k);
+            const float *pk = reinterpret_cast<const float *>(__shfl_sync(FULL, (unsigned long long)p, k));
+            if (!((there >> k) & 1u)) continue;
+            const float4 v = *reinterpret_cast<const float4 *>(pk + 4 + 4 * lane);
+            acc.x += v.x * fk;
+            acc.y += v.y * fk;
+            acc.z += v.z * fk;
+            acc.w += v.w * fk;
         }
-    };
-    if (a.prefix_tiles) {
-        const int r = b * a.G + g;
-        const bool rep = a.rows <= PA_REP_ROWS;
-        const int rt = r / (128 * MT);
-        take(head * w.per_head + (int64_t)rt * a.prefix_tiles, a.prefix_tiles, a.part_prefix,
-             (int64_t)head * a.row_tiles + rt, a.prefix_slot_rows, rep ? r : r % (128 * MT), rep ? 4 : 1, a.rows);
     }
-    take(head * w.per_head + (int64_t)a.row_tiles * a.prefix_tiles + before, own_tiles(a, b), a.part_own,
-         (int64_t)head * a.B + b, a.own_slot_rows, g, 4, a.G);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const size_t at = (size_t)row * PA_D + 4 * lane;
     if (out_dtype == HQMQ_BF16)
@@ -1101,15 +1142,11 @@ inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len,
     return p;
 }
 
-template <int RK, int RV, int MT> inline size_t attn_smem_bytes(uint32_t sk, uint32_t sv) {
-    return attn_table_end<RK, RV>(sk, sv) + sizeof(Shared<MT>);
-}
-
-template <int BT, int RK, int RV, int MT, int NT>
-static int launch_paged_attn(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
-                             cudaStream_t stream) {
-    const size_t smem = attn_smem_bytes<RK, RV, MT>(a.k.S, a.v.S);
-    auto kern = k_paged_attn<BT, RK, RV, MT, NT>;
+template <int BT, int MT, int NT>
+static int launch_paged_attn_b(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
+                               cudaStream_t stream) {
+    const size_t smem = attn_table_end(a.k.S, a.copies_k, a.v.S, a.copies_v) + sizeof(Shared<MT>);
+    auto kern = k_paged_attn<BT, MT, NT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
     const int64_t rows = (int64_t)a.B * a.Hk * a.G;
@@ -1121,16 +1158,17 @@ static int launch_paged_attn(const PagedAttnArgs &a, int ctas, void *o, int out_
 }
 
 template <int MT, int NT>
-static int launch_paged_attn_mt(const PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse,
-                                cudaStream_t stream) {
-    // the index widths of S = 8 and S = 32; 8 table copies (no bank conflicts) where they fit
-    const bool same = a.k.b == a.v.b;
-    if (same && a.k.b == 8) return launch_paged_attn<8, 8, 8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
-    if (same && a.k.b == 10)
-        return attn_smem_bytes<8, 4, MT>(a.k.S, a.v.S) <= 227 * 1024
-                   ? launch_paged_attn<10, 8, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream)
-                   : launch_paged_attn<10, 4, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
-    return launch_paged_attn<0, 4, 4, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+static int launch_paged_attn(PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse, cudaStream_t stream) {
+    // 8 table copies (no bank conflicts) where they fit, K's first
+    const auto fits = [&](uint32_t rk, uint32_t rv) {
+        return attn_table_end(a.k.S, rk, a.v.S, rv) + sizeof(Shared<MT>) <= 227 * 1024;
+    };
+    a.copies_k = fits(8, 4) ? 8 : 4;
+    a.copies_v = fits(a.copies_k, 8) ? 8 : 4;
+    // the index widths of S = 8 and S = 32 are compiled in
+    if (a.k.b == a.v.b && a.k.b == 8) return launch_paged_attn_b<8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+    if (a.k.b == a.v.b && a.k.b == 10) return launch_paged_attn_b<10, MT, NT>(a, ctas, o, out_dtype, lse, stream);
+    return launch_paged_attn_b<0, MT, NT>(a, ctas, o, out_dtype, lse, stream);
 }
 
 }  // namespace hqmq
@@ -1169,7 +1207,8 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
     a.row_tiles = p.row_tiles;
     a.prefix_tiles = (prefix_len + PA_TILE - 1) / PA_TILE;
     const double sl2 = (double)scale * 1.4426950408889634;
-    a.sl2 = (float)(sl2 < 0 ? -sl2 : sl2);
+    a.sl2 = fmaxf((float)(sl2 < 0 ? -sl2 : sl2), 1.2e-38f);  // (above 0, so that -inf stays -inf)
+    a.prefix_cost = a.rows <= PA_REP_ROWS ? OWN_COST : OWN_COST;
     a.q_flip = scale < 0 ? 0x80008000u : 0u;
     a.part_prefix = reinterpret_cast<float *>(ws);
     a.part_own = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + p.prefix_bytes);
@@ -1180,7 +1219,7 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
     const int64_t most = a.Hk * ((int64_t)a.row_tiles * a.prefix_tiles +
                                  (int64_t)B * (((int64_t)max_pages * k->page_size + PA_TILE - 1) / PA_TILE));
     const int ctas = (int)(most < PA_CTAS ? most : PA_CTAS);
-    if (out_dtype == HQMQ_F32) return launch_paged_attn_mt<1, 3>(a, ctas, o, out_dtype, lse, stream);
-    return p.mt == 2 ? launch_paged_attn_mt<2, 2>(a, ctas, o, out_dtype, lse, stream)
-                     : launch_paged_attn_mt<1, 2>(a, ctas, o, out_dtype, lse, stream);
+    if (out_dtype == HQMQ_F32) return launch_paged_attn<1, 3>(a, ctas, o, out_dtype, lse, stream);
+    return p.mt == 2 ? launch_paged_attn<2, 2>(a, ctas, o, out_dtype, lse, stream)
+                     : launch_paged_attn<1, 2>(a, ctas, o, out_dtype, lse, stream);
 }

@@ -125,7 +125,11 @@ def run(rng, B, Hk, G, page, S, cap, lens, prefix, out=torch.float32, scale=None
     (20, 1, 7, 16, 3, 25, list(range(20)), 300, torch.float32),        # 140 rows: more than one tile of them
     (5, 1, 1, 128, 11, 256, [3, 9, 1, 0, 250], 1000, torch.float32),
     (2, 1, 3, 256, 1, 500, [257, 2], 511, torch.bfloat16),
-    (33, 1, 8, 32, 32, 64, [1] * 33, 400, torch.float32)])             # 264 rows
+    (33, 1, 8, 32, 32, 64, [1] * 33, 400, torch.float32),              # 264 rows
+    (33, 2, 8, 64, 32, 128, [1, 70, 0] * 11, 700, torch.bfloat16),     # and in bf16: two groups of 128 at once
+    (20, 1, 7, 16, 8, 0, [65, 3] * 10, 3, torch.bfloat16),
+    (18, 5, 16, 32, 32, 64, list(range(18)), 200, torch.bfloat16),     # 288 rows: a second pair that is mostly empty
+    (40, 1, 8, 64, 20, 128, [0] * 40, 129, torch.bfloat16)])           # another index width, prefix only
 def test_against_plain_attention(B, Hk, G, page, S, cap, lens, prefix, out):
     run(np.random.default_rng(B * 100 + G), B, Hk, G, page, S, cap, lens, prefix, out)
 
