@@ -15,9 +15,8 @@
 //   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // k_paged_attn, warps by role:
-//   * one scout warp looks the tiles' pages up (page ids two tiles ahead,
-//     flag words one) and tells the producers where each token's codes and
-//     flagged values lie;
+//   * three scout warps look the tiles' pages and flag words up and tell the
+//     producers where each token's codes and flagged values lie;
 //   * 16 producer warps, 8 for K and 8 for V, decode a tile's codes from
 //     global memory (fetched a tile ahead) through the head's codeword table
 //     in shared memory into bf16 tiles [64 tokens][128]
@@ -49,8 +48,8 @@ constexpr int PA_REP_ROWS = 32;               // segments up to this many rows a
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
 constexpr int META_RING = 4;                  // tiles
-constexpr int MASK_RING = 16;                 // the scout is at most 10 tiles ahead of the softmax
-constexpr int PROD_WARPS = 16;
+constexpr int MASK_RING = 16;                 // the scouts are at most 10 tiles ahead of the softmax
+constexpr int PROD_WARPS = 16, SCOUTS = 3;
 
 struct PagedAttnArgs {
     const uint16_t *q;
@@ -157,7 +156,7 @@ template <int MT> struct Rows {
     __device__ __forceinline__ int groups() const { return rep ? 1 : (n + 127) / 128; }
 };
 
-// What the scout warp finds out about a tile.
+// What a scout warp finds out about a tile.
 struct Meta {
     long long page[PA_TILE / 16];             // page * heads + head of every 16 tokens
     int row0, head;                           // row of the first token in its page
@@ -222,31 +221,42 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------
-// scout: one warp, lane l = tokens 2 l and 2 l + 1 of the tile
+// scouts: warp s takes every third tile, lane l = its tokens 2 l and 2 l + 1
 // ---------------------------------------------------------------------------
-// Page ids are fetched two tiles before the tile is handed on, flag words one.
+// A tile's page ids are fetched two of the warp's tiles before it is handed
+// on, its flag words one.
 struct Scout {
     const PagedAttnArgs &a;
     const int lane;
     Cursor c;
-    bool first;                               // the cursor's tile is the first of a piece
-    int len;                                  // tokens of its segment
+    int len;                                  // tokens of the cursor's segment
     const int *tab;                           // and its pages
-    uint32_t base;                            // flagged chunks before the next tile in its page, K | V << 16
 
     struct Tile {
         int head, t0, n, page;                // head < 0: none; n tokens
-        bool first;
         uint2 fk, fv;
+        uint32_t before;                      // flagged chunks in the page's earlier rows, this lane's, K | V << 16
     };
 
-    __device__ __forceinline__ Scout(const PagedAttnArgs &a_, const Cursor &c_, int lane_)
-        : a(a_), lane(lane_), c(c_), first(true), base(0) { segment(); }
+    __device__ __forceinline__ Scout(const PagedAttnArgs &a_, const Cursor &c_, int lane_, int first)
+        : a(a_), lane(lane_), c(c_) {
+        segment();
+        step(first);
+    }
     __device__ __forceinline__ void segment() {
         const bool pre = c.prefix(a);
         const int b = c.seg - a.row_tiles;
         len = c.left <= 0 ? 0 : pre ? a.prefix_len : own_len(a, b);
         tab = pre ? a.prefix_table : a.table + (size_t)b * a.max_pages;
+    }
+    __device__ __forceinline__ void step(int n) {
+        for (; n > 0 && c.left > 0; --n) {
+            c.left -= c.cost(a);
+            if (++c.tile >= c.n_tiles) {
+                c.settle(a);
+                segment();
+            }
+        }
     }
 
     __device__ __forceinline__ void pages(Tile &x) {
@@ -255,39 +265,39 @@ struct Scout {
         x.head = c.head;
         x.t0 = c.tile * PA_TILE;
         x.n = min(len - x.t0, PA_TILE);
-        x.first = first;
         x.page = -2;                          // no token
         if (2 * lane < x.n) x.page = __ldg(tab + ((x.t0 + 2 * lane) >> a.k.page_shift));
-        c.left -= c.cost(a);
-        first = ++c.tile >= c.n_tiles;
-        if (first) {
-            c.settle(a);
-            segment();
-        }
+        step(SCOUTS);
     }
     __device__ __forceinline__ void flags(Tile &x) {
         x.fk = x.fv = make_uint2(0u, 0u);
+        x.before = 0u;
         if (x.head < 0) return;
         if (x.page != -2 && (x.page < 0 || x.page >= a.k.n_pages || x.page >= a.v.n_pages)) {
             if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
             x.page = -1;
         }
+        const int row0 = x.t0 & (a.k.page_size - 1);
+        const int pg0 = __shfl_sync(FULL, x.page, 0);
         if (x.page >= 0) {
             const size_t at = a.k.at(x.page, x.head, (x.t0 + 2 * lane) & (a.k.page_size - 1));
             if (a.k.flags) x.fk = __ldg(reinterpret_cast<const uint2 *>(a.k.flags + at));
             if (a.v.flags) x.fv = __ldg(reinterpret_cast<const uint2 *>(a.v.flags + at));
             if (2 * lane + 1 >= x.n) x.fk.y = x.fv.y = 0u;
         }
+        if (row0 > 0 && pg0 >= 0) {           // pages of 128 or 256 tokens: the rows before the tile's
+            const size_t at = a.k.at(pg0, x.head, 2 * lane);
+            for (int r = 0; r < row0; r += PA_TILE) {
+                uint2 k = make_uint2(0u, 0u), v = k;
+                if (a.k.flags) k = __ldg(reinterpret_cast<const uint2 *>(a.k.flags + at + r));
+                if (a.v.flags) v = __ldg(reinterpret_cast<const uint2 *>(a.v.flags + at + r));
+                x.before += (__popc(k.x) + __popc(k.y)) | ((__popc(v.x) + __popc(v.y)) << 16);
+            }
+        }
     }
     __device__ __forceinline__ void hand_on(const Tile &x, Meta &m, uint2 *mask) {
         const int row0 = x.t0 & (a.k.page_size - 1);
-        if (row0 == 0) base = 0;
-        else if (x.first) {                   // a piece that starts inside a page
-            const int pg = __shfl_sync(FULL, x.page, 0);
-            const size_t f = pg >= 0 ? a.k.at(pg, x.head, 0) : 0;
-            base = pg >= 0 && a.k.flags ? flags_before(a.k.flags + f, row0, lane) : 0u;
-            if (pg >= 0 && a.v.flags) base |= flags_before(a.v.flags + f, row0, lane) << 16;
-        }
+        const uint32_t base = row0 > 0 ? __reduce_add_sync(FULL, x.before) : 0u;
         const uint32_t n0 = __popc(x.fk.x) | (__popc(x.fv.x) << 16);
         const uint32_t n = n0 + (__popc(x.fk.y) | (__popc(x.fv.y) << 16));
         uint32_t inc = n;
@@ -299,7 +309,6 @@ struct Scout {
         // slots start anew with every page: 8, 16 or more lanes
         const uint32_t before = __shfl_sync(FULL, inc - n, lane & ~((a.k.page_size >> 1) - 1) & 31);
         const uint32_t start = base + (inc - n) - before;
-        base += __shfl_sync(FULL, inc, 31);
         m.flags[0][lane] = x.fk;
         m.flags[1][lane] = x.fv;
         m.start[0][lane] = (start & 0xFFFFu) | ((start + n0) << 16);
@@ -322,21 +331,22 @@ struct Scout {
 };
 
 template <int MT>
-__device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int lane) {
-    Scout s(a, sh.start, lane);
+__device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int which, int lane) {
+    Scout s(a, sh.start, lane, which);
     const int total = sh.total;
     Scout::Tile x[2];
     s.pages(x[0]);
     s.pages(x[1]);
     s.flags(x[0]);
-    for (int n = 0; n < total; n += 2) {
+    for (int n = which; n < total; n += 2 * SCOUTS) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (n + i >= total) break;
-            const int slot = (n + i) % META_RING;
+            const int t = n + i * SCOUTS;
+            if (t >= total) break;
+            const int slot = t % META_RING;
             s.flags(x[1 - i]);
-            if (!mbar_wait(&sh.meta_empty[slot], (((n + i) / META_RING) & 1) ^ 1)) return false;
-            s.hand_on(x[i], sh.meta[slot], &sh.mask[(n + i) % MASK_RING]);
+            if (!mbar_wait(&sh.meta_empty[slot], ((t / META_RING) & 1) ^ 1)) return false;
+            s.hand_on(x[i], sh.meta[slot], &sh.mask[t % MASK_RING]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_full[slot]);
             s.pages(x[i]);
@@ -660,6 +670,13 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
         : "=f"(o.x), "=f"(o.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return o;
 }
+__device__ __forceinline__ float2 sub_pair(float2 a, float2 b) {     // a + (-1) b: no sign flips beside it
+    float2 o;
+    asm("{.reg .b64 t, u, v;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 u, {%4, %5};\n\tmov.b64 v, {%6, %6};\n\t"
+        "fma.rn.f32x2 t, u, v, t;\n\tmov.b64 {%0, %1}, t;}"
+        : "=f"(o.x), "=f"(o.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(-1.0f));
+    return o;
+}
 __device__ __forceinline__ float2 bf16_pair(uint32_t h) {
     return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
 }
@@ -679,7 +696,7 @@ __device__ __forceinline__ void weights(const uint32_t *s, float sl2, float ref,
             out[t][j / 2] = h;
             if (t + 1 < NT) {
                 const float2 f = bf16_pair(h);
-                p = add_pair(p, make_float2(-f.x, -f.y));
+                p = sub_pair(p, f);
             }
         }
     }
@@ -906,13 +923,12 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     return true;
 }
 
-// Warps: 4 MT softmax, 16 producers, the scout, the products and two that
-// only fill the last group of four, which shares registers as a whole: the
-// block is launched with REGS a thread, and each role takes what it needs of
-// their sum.
+// Warps: 4 MT softmax, 16 producers, three scouts, the products.  The block is
+// launched with REGS a thread, and each group of four warps takes what it
+// needs of their sum.
 template <int MT> struct Roles {
-    static constexpr int SCOUT = 4 * MT + PROD_WARPS;
-    static constexpr int THREADS = (SCOUT + 4) * 32;
+    static constexpr int SCOUT = 4 * MT + PROD_WARPS, PRODUCTS = SCOUT + SCOUTS;
+    static constexpr int THREADS = (PRODUCTS + 1) * 32;
     static constexpr int REGS = MT == 1 ? 80 : 72;
     static constexpr int SOFTMAX = MT == 1 ? 128 : 80, PRODUCER = 72, REST = MT == 1 ? 64 : 56;
     static_assert(REGS * THREADS <= 65536, "registers of an SM");
@@ -923,12 +939,12 @@ template <int N> __device__ __forceinline__ void regs_down() { asm volatile("set
 
 template <int BT, int MT, int NT>
 __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __grid_constant__ PagedAttnArgs a) {
-    constexpr int SCOUT = Roles<MT>::SCOUT;
+    constexpr int SCOUT = Roles<MT>::SCOUT, PRODUCTS = Roles<MT>::PRODUCTS;
     extern __shared__ __align__(1024) uint8_t dyn[];   // (the swizzle's period)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tiles = smem_addr(dyn), tables = tiles + 4 * TILE_BYTES;
     Shared<MT> &sh = *reinterpret_cast<Shared<MT> *>(dyn + attn_table_end(a.k.S, a.copies_k, a.v.S, a.copies_v));
-    if (warp == SCOUT + 1) {
+    if (warp == PRODUCTS) {
         tmem_alloc(&sh.tmem, Tmem<MT, NT>::COLS);
         if (lane == 0) {
             sh.failed = 0;
@@ -1024,9 +1040,9 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         ok = produce<BT, MT>(a, sh, tables, tiles, warp - 4 * MT, lane);
     } else {
         regs_down<Roles<MT>::REST>();
-        if (warp == SCOUT) {
-            ok = scout<MT>(a, sh, lane);
-        } else if (warp == SCOUT + 1) {
+        if (warp < PRODUCTS) {
+            ok = scout<MT>(a, sh, warp - SCOUT, lane);
+        } else {
             const bool leader = elect_one();
             ok = issue_products<MT, NT>(a, sh, tiles, leader);
             if (leader) mma_commit(&sh.drain);    // nothing may be in flight when tensor memory goes
@@ -1036,7 +1052,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
     if (!ok) sh.failed = 1;
     tc_fence_before();
     __syncthreads();
-    if (warp == SCOUT + 1) {
+    if (warp == PRODUCTS) {
         tc_fence_after();
         tmem_free(sh.tmem, Tmem<MT, NT>::COLS);
     }
@@ -1220,6 +1236,6 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
                                  (int64_t)B * (((int64_t)max_pages * k->page_size + PA_TILE - 1) / PA_TILE));
     const int ctas = (int)(most < PA_CTAS ? most : PA_CTAS);
     if (out_dtype == HQMQ_F32) return launch_paged_attn<1, 3>(a, ctas, o, out_dtype, lse, stream);
-    return p.mt == 2 ? launch_paged_attn<2, 2>(a, ctas, o, out_dtype, lse, stream)
-                     : launch_paged_attn<1, 2>(a, ctas, o, out_dtype, lse, stream);
+    return p.mt == 2 ? launch_paged_attn<2, 1>(a, ctas, o, out_dtype, lse, stream)
+                     : launch_paged_attn<1, 1>(a, ctas, o, out_dtype, lse, stream);
 }
