@@ -17,9 +17,9 @@
 // k_paged_attn, warps by role:
 //   * three scout warps look the tiles' pages and flag words up and tell the
 //     producers where each token's codes and flagged values lie;
-//   * 16 producer warps, 8 for K and 8 for V, decode a tile's codes from
-//     global memory (fetched a tile ahead) through the head's codeword table
-//     in shared memory into bf16 tiles [64 tokens][128]
+//   * 16 producer warps decode codes from global memory (fetched two tiles
+//     ahead) through the head's codeword table in shared memory into bf16
+//     tiles [64 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
 //   * one warp's elected thread issues the products (tcgen05.mma, 128 rows, accumulators
@@ -175,7 +175,7 @@ template <int MT> struct Shared {
     Meta meta[META_RING];
     uint2 mask[MASK_RING];                              // valid tokens of the last tiles
     Cursor start;
-    int total;                                          // tiles of the share
+    int total, last_head;                               // tiles of the share, and the last one's head
     uint32_t tmem;
     int failed;
 };
@@ -380,16 +380,16 @@ __device__ __forceinline__ void build_table(const PagesDev &p, uint32_t R, int h
     }
 }
 
-// Words that hold a lane's 8 indices (bits 8 q b .. 8 q b + 8 b - 1).
-template <int BT> struct RunWords { static constexpr int N = BT == 8 ? 2 : BT == 10 ? 3 : 4; };
+// Words that hold a lane's 16 indices (bits 16 h b .. 16 h b + 16 b - 1).
+template <int BT> struct RunWords { static constexpr int N = BT == 8 ? 4 : BT == 10 ? 5 : 6; };
 
-// One tile's codes on their way: lane (q, token) = (lane / 8, 8 sub + lane %
-// 8) decodes chunks 8 q .. 8 q + 7 of that token.
+// One tile's codes on their way: lane (h, token) = (lane / 16, 16 sub + lane
+// % 16) decodes chunks 16 h .. 16 h + 15 of that token.
 template <int BT> struct Slot {
     int head;
-    uint4 rad;
+    uint4 rad[2];
     uint32_t w[RunWords<BT>::N];
-    uint32_t f8;                              // flagged chunks among this lane's
+    uint32_t flagged;                         // flagged chunks among this lane's
     int slot;                                 // slot of the first of them
     uint2 val;                                // and its value
     const uint2 *slots;
@@ -397,57 +397,59 @@ template <int BT> struct Slot {
 
 template <int BT> struct Producer {
     const PagesDev &p;
-    const int lane, q, tok, which;
+    const int lane, h, tok, which;
     const uint32_t stride, copy;              // bytes of a table entry, this lane's copy in the table
+    const uint32_t row;                       // this lane's 128 bytes in a tile, its swizzle in bits 4 - 6
 
     __device__ __forceinline__ Producer(const PagesDev &p_, int which_, int sub, int lane_, uint32_t R, uint32_t table)
-        : p(p_), lane(lane_), q(lane_ >> 3), tok(sub * 8 + (lane_ & 7)), which(which_), stride(R * 16u),
-          copy(table + (lane_ & (R - 1u)) * 16u) {}
+        : p(p_), lane(lane_), h(lane_ >> 4), tok(sub * 16 + (lane_ & 15)), which(which_), stride(R * 16u),
+          copy(table + (lane_ & (R - 1u)) * 16u),
+          row(h * (TILE_BYTES / 2) + (tok >> 3) * 1024 + (tok & 7) * 128 + (tok & 7) * 16) {}
 
     __device__ __forceinline__ void fetch(Slot<BT> &s, const Meta &m) {
         s.head = m.head;
-        s.rad = make_uint4(0u, 0u, 0u, 0u);
+        s.rad[0] = s.rad[1] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < RunWords<BT>::N; ++i) s.w[i] = 0u;
-        s.f8 = 0u;
+        s.flagged = 0u;
         if (!((m.mask[tok >> 5] >> (tok & 31)) & 1u)) return;
         const long long ph = m.page[tok >> 4];
         const size_t at = ((size_t)ph << p.page_shift) + ((m.row0 + tok) & (p.page_size - 1));
-        s.rad = __ldg(reinterpret_cast<const uint4 *>(p.radius + at * PG_CHUNKS) + q);
-        const uint32_t b = BT ? BT : p.b, wo = (8u * q * b) >> 5;
+        const uint4 *rad = reinterpret_cast<const uint4 *>(p.radius + at * PG_CHUNKS) + 2 * h;
+        s.rad[0] = __ldg(rad);
+        s.rad[1] = __ldg(rad + 1);
+        const uint32_t b = BT ? BT : p.b, wo = (h * b) >> 1;
         const uint32_t *w = p.words + at * b + wo;
 #pragma unroll
         for (int i = 0; i < RunWords<BT>::N; ++i)
             if (BT || wo + i < b) s.w[i] = __ldg(w + i);
         const uint32_t f = reinterpret_cast<const uint32_t *>(m.flags[which])[tok];
-        s.f8 = (f >> (8 * q)) & 0xFFu;
-        s.slot = reinterpret_cast<const uint16_t *>(m.start[which])[tok] + __popc(f & ((1u << (8 * q)) - 1u));
+        s.flagged = (f >> (16 * h)) & 0xFFFFu;
+        s.slot = reinterpret_cast<const uint16_t *>(m.start[which])[tok] + (h ? __popc(f & 0xFFFFu) : 0);
         s.slots = reinterpret_cast<const uint2 *>(p.val) + (size_t)ph * p.cap;
-        if (s.f8 && s.slot < p.cap) s.val = __ldg(s.slots + s.slot);
+        if (s.flagged && s.slot < p.cap) s.val = __ldg(s.slots + s.slot);
     }
 
-    // The lane's 8 chunks to the tile, then the flagged ones over them.
+    // The lane's 16 chunks to the tile, then the flagged ones over them.
     __device__ __forceinline__ void decode(const Slot<BT> &s, uint32_t tile) {
         constexpr int N = RunWords<BT>::N;
-        const uint32_t b = BT ? BT : p.b, sh = (8u * q * b) & 31u;
+        const uint32_t b = BT ? BT : p.b, sh = BT ? 0u : ((h * b) & 1u) * 16u;
         uint32_t x[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            x[i] = BT == 8 ? s.w[i] : i + 1 < N ? __funnelshift_r(s.w[i], s.w[i + 1], sh) : s.w[i] >> sh;
-        const uint32_t zero = 24u * p.S;
-        const uint32_t row = tile + (q >> 1) * (TILE_BYTES / 2) + (tok >> 3) * 1024 + (tok & 7) * 128;
-        const uint32_t u0 = (q & 1) * 4, swz = tok & 7;
+            x[i] = BT ? s.w[i] : i + 1 < N ? __funnelshift_r(s.w[i], s.w[i + 1], sh) : s.w[i] >> sh;
+        const uint32_t zero = 24u * p.S, to = tile + row;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int g = 0; g < 4; ++g) {
             float4 c[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int j = 4 * h + k;
+                const int j = 4 * g + k;
                 uint32_t v;                   // the index, other bits above it
                 if (BT) {
                     constexpr int BB = BT ? BT : 1;
                     const int pos = j * BB, wi = pos >> 5, s5 = pos & 31;
-                    if (s5 + BB > 32 && wi + 1 < N) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5);
+                    if (s5 + BB > 32) v = __funnelshift_r(x[wi], x[wi + 1 < N ? wi + 1 : wi], s5);
                     else v = x[wi] >> s5;
                 } else {
                     const uint32_t pos = j * b, wi = pos >> 5, s5 = pos & 31u;
@@ -462,27 +464,28 @@ template <int BT> struct Producer {
                 }
                 c[k] = lds128(min(v & ((1u << b) - 1u), zero) * stride + copy);
             }
+            const uint4 r4 = s.rad[g >> 1];
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
-                const uint32_t rw = h == 0 ? (k == 0 ? s.rad.x : s.rad.y) : (k == 0 ? s.rad.z : s.rad.w);
+                const uint32_t rw = g & 1 ? (k ? r4.w : r4.z) : (k ? r4.y : r4.x);
                 const float r0 = f16_bits_to_f32(rw & 0xFFFFu), r1 = f16_bits_to_f32(rw >> 16);
                 const float2 y0 = mul_pair(r0, c[k].x, c[k].y), y1 = mul_pair(r0, c[k].z, c[k].w);
                 const float2 y2 = mul_pair(r1, c[k + 1].x, c[k + 1].y), y3 = mul_pair(r1, c[k + 1].z, c[k + 1].w);
-                sts128(row + ((u0 + 2 * h + (k >> 1)) ^ swz) * 16, bf16x2(y0.x, y0.y), bf16x2(y1.x, y1.y),
-                       bf16x2(y2.x, y2.y), bf16x2(y3.x, y3.y));
+                sts128(to ^ ((2 * g + (k >> 1)) * 16), bf16x2(y0.x, y0.y), bf16x2(y1.x, y1.y), bf16x2(y2.x, y2.y),
+                       bf16x2(y3.x, y3.y));
             }
         }
-        uint32_t f8 = s.f8;
+        uint32_t f = s.flagged;
         uint2 v = s.val;
         int slot = s.slot;
-        while (f8 && slot < p.cap) {
-            const int j = __ffs(f8) - 1;
-            f8 &= f8 - 1u;
-            sts64(row + ((u0 + (j >> 1)) ^ swz) * 16 + (j & 1) * 8,
+        while (f && slot < p.cap) {
+            const int j = __ffs(f) - 1;
+            f &= f - 1u;
+            sts64((to ^ ((j >> 1) * 16)) + (j & 1) * 8,
                   bf16x2(f16_bits_to_f32(v.x & 0xFFFFu), f16_bits_to_f32(v.x >> 16)),
                   bf16x2(f16_bits_to_f32(v.y & 0xFFFFu), f16_bits_to_f32(v.y >> 16)));
             ++slot;
-            if (f8 && slot < p.cap) v = __ldg(s.slots + slot);
+            if (f && slot < p.cap) v = __ldg(s.slots + slot);
         }
     }
 };
@@ -494,46 +497,58 @@ __device__ __forceinline__ bool meet(uint64_t &bar, int &times, int lane) {
     return mbar_wait(&bar, times++ & 1);
 }
 
-// Warps 0-7 decode K, 8-15 V, eight tokens each.  A tile's codes are fetched
-// before the one before it is decoded.
+// Warps 0-7 take the even tiles, 8-15 the odd ones; of each eight, four
+// decode K and four V, sixteen tokens each.  A tile's codes are fetched before
+// the warp's last one is decoded.
 template <int BT, int MT>
 __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tables, uint32_t tiles,
                                         int warp, int lane) {
-    const int which = warp >> 3, sub = warp & 7;
+    const int st = warp >> 3, which = (warp >> 2) & 1, sub = warp & 3;
     const PagesDev &p = which ? a.v : a.k;
     const uint32_t R = which ? a.copies_v : a.copies_k;
     const uint32_t table = tables + (which ? table_bytes(a.k.S, a.copies_k) : 0u);
     Producer<BT> pr(p, which, sub, lane, R, table);
-    const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u);
-    uint64_t *full = which ? sh.v_full : sh.k_full, *empty = which ? sh.v_empty : sh.k_empty;
-    const int total = sh.total;
-    int head = -1, meetings = 0;
+    const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u) + st * TILE_BYTES;
+    uint64_t *full = (which ? sh.v_full : sh.k_full) + st, *empty = (which ? sh.v_empty : sh.k_empty) + st;
+    const int total = sh.total, last_head = sh.last_head;
+    int head = sh.start.head - 1, meetings = 0;
+    uint32_t par = 1;                         // phase of `empty` to wait for
     Slot<BT> x, next;
 
-    next.head = -1;
+    next.head = head;
 #pragma unroll 1
-    for (int n = -1; n < total; ++n) {
+    for (int n = st - 2; n < total; n += 2) {
         x = next;
-        if (n + 1 < total) {
-            const int r = (n + 1) % META_RING;
-            if (!mbar_wait(&sh.meta_full[r], ((n + 1) / META_RING) & 1)) return false;
+        if (n + 2 < total) {
+            const int r = (n + 2) % META_RING;
+            if (!mbar_wait(&sh.meta_full[r], ((n + 2) / META_RING) & 1)) return false;
             pr.fetch(next, sh.meta[r]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
+        } else {
+            next.head = last_head;
+        }
+        // every producer passes through every head: they meet, build its tables and meet again
+        const int to = n < 0 ? head : x.head;
+        while (head < to) {
+            if (!meet(sh.heads, meetings, lane)) return false;
+            ++head;
+            build_table(p, R, head, table, (st * 4 + sub) * 32 + lane);
+            if (!meet(sh.heads, meetings, lane)) return false;
         }
         if (n < 0) continue;
-        if (x.head != head) {                 // every producer meets the new head at the same tile
-            if (!meet(sh.heads, meetings, lane)) return false;
-            head = x.head;
-            build_table(p, R, head, table, sub * 32 + lane);
-            if (!meet(sh.heads, meetings, lane)) return false;
-        }
-        const int st = n & 1;
-        if (!mbar_wait(empty + st, ((n >> 1) & 1) ^ 1)) return false;
-        pr.decode(x, tile + st * TILE_BYTES);
+        if (!mbar_wait(empty, par)) return false;
+        par ^= 1u;
+        pr.decode(x, tile);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + st);
+        if (lane == 0) mbar_arrive(full);
+    }
+    while (head < last_head) {
+        if (!meet(sh.heads, meetings, lane)) return false;
+        ++head;
+        build_table(p, R, head, table, (st * 4 + sub) * 32 + lane);
+        if (!meet(sh.heads, meetings, lane)) return false;
     }
     return true;
 }
@@ -949,8 +964,8 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         if (lane == 0) {
             sh.failed = 0;
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sh.k_full[i], PROD_WARPS / 2);
-                mbar_init(&sh.v_full[i], PROD_WARPS / 2);
+                mbar_init(&sh.k_full[i], PROD_WARPS / 4);
+                mbar_init(&sh.v_full[i], PROD_WARPS / 4);
                 mbar_init(&sh.k_empty[i], 1);
                 mbar_init(&sh.v_empty[i], 1);
             }
@@ -965,7 +980,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             }
             for (int i = 0; i < META_RING; ++i) {
                 mbar_init(&sh.meta_full[i], 1);
-                mbar_init(&sh.meta_empty[i], PROD_WARPS);
+                mbar_init(&sh.meta_empty[i], PROD_WARPS / 2);
             }
             mbar_init(&sh.pair_done, 4);
             mbar_init(&sh.heads, PROD_WARPS);
@@ -1018,13 +1033,17 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             c.left -= (int64_t)c.tile * cost - at;
             c.settle(a);
         }
-        int total = 0;                        // tiles of the share
+        int total = 0, last = c.head - 1;
         for (Cursor d = c; d.left > 0;) {
             const int n = d.piece(a);
             total += n;
+            last = d.head;
             d.skip(a, n);
         }
-        if (lane == 0) sh.total = total;
+        if (lane == 0) {
+            sh.total = total;
+            sh.last_head = last;
+        }
         if (lane == 0) sh.start = c;
     }
     tc_fence_before();
