@@ -1,14 +1,24 @@
 // norm_rope.cu -- RMS norm of query and key head vectors with the position
 // rotation, in one pass (include/hqmq.h, hqmq_qk_norm_rope).
 //
-// One CTA takes one token: the R / 2 angles are computed once, in fp64, and
-// serve all of its heads; then a warp takes one head vector at a time.
+// A CTA takes one or a few tokens; their R / 2 angles are computed once, in
+// fp64, into shared memory and serve all heads.  The first vectors are loaded
+// before the angles, so that both latencies run at the same time.
+//
+// k_norm_rope: a lane takes 16 elements of a vector as two runs of 8 that are
+// rotated with each other (or 16 neighbours, when pairs are neighbours or
+// pass through), LPV lanes a vector: 16-byte accesses, the partner of every
+// element in the same lane, log2(LPV) shuffles for the norm.  It needs R and
+// D - R to be multiples of 16 and 16-byte aligned vectors; k_norm_rope_any
+// (a warp per vector, element by element) takes every other call.
 #include "hqmq_device.cuh"
 
 namespace hqmq {
 
-constexpr int NR_WARPS = 8;
 constexpr int NR_MAX_D = 512;
+constexpr int NR_ANY_WARPS = 8;
+constexpr int NR_THREADS = 512;
+constexpr int NR_MAX_ANGLES = 1024;           // of the tokens of a CTA
 
 struct NormRopeArgs {
     const void *in[2];
@@ -39,10 +49,154 @@ template <typename E> __device__ __forceinline__ E from_f32(float v);
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
+// Eight neighbouring elements, 16-byte aligned.
+template <typename E> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float *f) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(void *p, const float *f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void get(float *f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(void *p, const float *f) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+// A CTA takes a span of tokens and blockDim.x / LPV heads (blockIdx.y: which);
+// a thread stays with its 16 elements of its head, so the weights stay in
+// registers, and walks the tokens, loading the next one's elements before it
+// works on the current one's.
+template <typename E, int LPV, bool PAIRS>
+__global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const __grid_constant__ NormRopeArgs a, unsigned tokens,
+                                                          int span) {
+    __shared__ __align__(16) float2 s_cs[NR_MAX_ANGLES];
+    pdl_wait();
+    pdl_trigger();
+    const unsigned t0 = blockIdx.x * span;
+    const int n_tok = (int)min((unsigned)span, tokens - t0);
+    const int half = a.R / 2, total = a.heads[0] + a.heads[1];
+    const int part = threadIdx.x & (LPV - 1);     // which 16 elements
+    // element offsets of the two runs of 8
+    const bool rot = part * 16 < a.R, split = rot && !PAIRS;
+    const int e0 = split ? part * 8 : part * 16, e1 = split ? half + part * 8 : part * 16 + 8;
+    const int hh = blockIdx.y * (blockDim.x / LPV) + threadIdx.x / LPV;
+    const bool on = hh < total && part * 16 < a.D;
+    const bool is_k = hh >= a.heads[0];
+    const int h = is_k ? hh - a.heads[0] : hh;
+    const int64_t it = is_k ? a.it[1] : a.it[0], ot = is_k ? a.ot[1] : a.ot[0];
+    const int64_t ib = is_k ? a.ib[1] : a.ib[0], ob = is_k ? a.ob[1] : a.ob[0];
+    unsigned bb = t0 / (unsigned)a.T, tt = t0 - bb * (unsigned)a.T;
+    const E *in = reinterpret_cast<const E *>(is_k ? a.in[1] : a.in[0]) + h * (is_k ? a.ih[1] : a.ih[0]) + bb * ib + tt * it;
+    E *out = reinterpret_cast<E *>(is_k ? a.out[1] : a.out[0]) + h * (is_k ? a.oh[1] : a.oh[0]) + bb * ob + tt * ot;
+    const void *w = is_k ? a.w[1] : a.w[0];
+
+    Raw8<E> r0 = {}, r1 = {};
+    if (on) {
+        r0.load(in + e0);
+        r1.load(in + e1);
+    }
+    float g[16];
+    if (on && w) {
+        if (a.w_f32) {
+            Raw8<float> q;
+            q.load(reinterpret_cast<const float *>(w) + e0);
+            q.get(g);
+            q.load(reinterpret_cast<const float *>(w) + e1);
+            q.get(g + 8);
+        } else {
+            Raw8<__nv_bfloat16> q;
+            q.load(reinterpret_cast<const __nv_bfloat16 *>(w) + e0);
+            q.get(g);
+            q.load(reinterpret_cast<const __nv_bfloat16 *>(w) + e1);
+            q.get(g + 8);
+        }
+    }
+    for (int i = threadIdx.x; i < n_tok * half; i += blockDim.x) {
+        const int k = i / half;
+        s_cs[i] = angle_cs(a.pos[t0 + k], a.inv_freq[i - k * half]);
+    }
+    __syncthreads();
+    const float inv_d = 1.0f / (float)a.D;
+    for (int k = 0; k < n_tok; ++k) {
+        float f[16];
+        r0.get(f);
+        r1.get(f + 8);
+        E *const y = out;
+        // the next token
+        in += it;
+        out += ot;
+        if (++tt == (unsigned)a.T) {
+            tt = 0;
+            in += ib - (int64_t)a.T * it;
+            out += ob - (int64_t)a.T * ot;
+        }
+        if (on && k + 1 < n_tok) {
+            r0.load(in + e0);
+            r1.load(in + e1);
+        }
+        float sum = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sum = fmaf(f[i], f[i], sum);
+            sum1 = fmaf(f[i + 8], f[i + 8], sum1);
+        }
+        sum += sum1;
+#pragma unroll
+        for (int o = LPV / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        if (!on) continue;
+        if (w) {
+            const float r = rsqrtf(sum * inv_d + a.eps);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = f[i] * r * g[i];
+        }
+        if (rot) {
+            const float4 *cs = reinterpret_cast<const float4 *>(s_cs + k * half + part * 8);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float4 c = cs[i / 2];       // pairs i and i + 1
+                constexpr int V = PAIRS ? 1 : 8, U = PAIRS ? 2 : 1;
+                const float p = f[i * U], q = f[i * U + V], r = f[(i + 1) * U], t = f[(i + 1) * U + V];
+                f[i * U] = p * c.x - q * c.y;
+                f[i * U + V] = q * c.x + p * c.y;
+                f[(i + 1) * U] = r * c.z - t * c.w;
+                f[(i + 1) * U + V] = t * c.z + r * c.w;
+            }
+        }
+        Raw8<E>::store(y + e0, f);
+        Raw8<E>::store(y + e1, f + 8);
+    }
+}
+
 template <typename E>
-__global__ void __launch_bounds__(NR_WARPS * 32) k_norm_rope(NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_ANY_WARPS * 32) k_norm_rope_any(NormRopeArgs a) {
     __shared__ float2 s_cs[NR_MAX_D / 2];
-    __shared__ float s_x[NR_WARPS][NR_MAX_D];
+    __shared__ float s_x[NR_ANY_WARPS][NR_MAX_D];
     pdl_wait();
     const int64_t token = blockIdx.x;
     const int64_t bb = token / a.T, tt = token % a.T;
@@ -51,7 +205,7 @@ __global__ void __launch_bounds__(NR_WARPS * 32) k_norm_rope(NormRopeArgs a) {
     for (int i = threadIdx.x; i < half; i += blockDim.x) s_cs[i] = angle_cs(a.pos[token], a.inv_freq[i]);
     __syncthreads();
     const int total = a.heads[0] + a.heads[1];
-    for (int hh = warp; hh < total; hh += NR_WARPS) {
+    for (int hh = warp; hh < total; hh += NR_ANY_WARPS) {
         const int s = hh >= a.heads[0];
         const int h = s ? hh - a.heads[0] : hh;
         const E *x = reinterpret_cast<const E *>(a.in[s]) + bb * a.ib[s] + tt * a.it[s] + h * a.ih[s];
@@ -66,7 +220,7 @@ __global__ void __launch_bounds__(NR_WARPS * 32) k_norm_rope(NormRopeArgs a) {
         if (w) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-            const float f = 1.0f / sqrtf(sum / (float)a.D + a.eps);
+            const float f = rsqrtf(sum / (float)a.D + a.eps);
             for (int d = lane; d < a.D; d += 32)
                 s_x[warp][d] *= f * (a.w_f32 ? reinterpret_cast<const float *>(w)[d]
                                              : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(w)[d]));
@@ -88,6 +242,36 @@ __global__ void __launch_bounds__(NR_WARPS * 32) k_norm_rope(NormRopeArgs a) {
     }
 }
 
+template <typename E, int LPV>
+static cudaError_t launch_norm_rope_lpv(const NormRopeArgs &a, unsigned tokens, cudaStream_t stream) {
+    // tokens of a CTA: up to 8 (their angles fit shared memory), so that the angles' latency is paid once
+    // for all of them, fewer where that would leave SMs idle
+    int span = 8;
+    while (span > 1 && (span * (a.R / 2) > NR_MAX_ANGLES || tokens / span < 4 * 148)) span /= 2;
+    // heads: all in one CTA if they fit, in equal shares otherwise; a few tokens spread theirs over the SMs
+    const int total = a.heads[0] + a.heads[1], most = (tokens < 148 ? 128 : NR_THREADS) / LPV;
+    const int shares = (total + most - 1) / most, heads = (total + shares - 1) / shares;
+    const dim3 g((tokens + span - 1) / span, shares), b((heads * LPV + 31) / 32 * 32);
+    return a.interleaved ? launch_pdl(k_norm_rope<E, LPV, true>, g, b, 0, stream, a, tokens, span)
+                         : launch_pdl(k_norm_rope<E, LPV, false>, g, b, 0, stream, a, tokens, span);
+}
+
+template <typename E>
+static cudaError_t launch_norm_rope(const NormRopeArgs &a, unsigned tokens, bool wide, cudaStream_t stream) {
+    if (!wide)
+        return launch_pdl(k_norm_rope_any<E>, dim3(tokens), dim3(NR_ANY_WARPS * 32), 0, stream, a);
+    int lpv = 1;
+    while (lpv * 16 < a.D) lpv *= 2;
+    switch (lpv) {
+        case 1: return launch_norm_rope_lpv<E, 1>(a, tokens, stream);
+        case 2: return launch_norm_rope_lpv<E, 2>(a, tokens, stream);
+        case 4: return launch_norm_rope_lpv<E, 4>(a, tokens, stream);
+        case 8: return launch_norm_rope_lpv<E, 8>(a, tokens, stream);
+        case 16: return launch_norm_rope_lpv<E, 16>(a, tokens, stream);
+        default: return launch_norm_rope_lpv<E, 32>(a, tokens, stream);
+    }
+}
+
 }  // namespace hqmq
 
 extern "C" int hqmq_launch_norm_rope(const hqmq_head_view *q, const hqmq_head_view *q_out,
@@ -99,6 +283,12 @@ extern "C" int hqmq_launch_norm_rope(const hqmq_head_view *q, const hqmq_head_vi
     NormRopeArgs a = {};
     const hqmq_head_view *in[2] = {q, k}, *out[2] = {q_out, k_out};
     const void *w[2] = {qw, kw};
+    const int64_t esz = dtype == HQMQ_BF16 ? 2 : 4;
+    bool wide = R % 16 == 0 && (D - R) % 16 == 0;
+    const auto aligned16 = [&](const hqmq_head_view *v) {
+        return reinterpret_cast<uintptr_t>(v->data) % 16 == 0 && v->stride_b * esz % 16 == 0 &&
+               v->stride_t * esz % 16 == 0 && v->stride_h * esz % 16 == 0;
+    };
     for (int s = 0; s < 2; ++s) {
         if (!in[s]) continue;
         a.in[s] = in[s]->data;
@@ -107,6 +297,7 @@ extern "C" int hqmq_launch_norm_rope(const hqmq_head_view *q, const hqmq_head_vi
         a.ob[s] = out[s]->stride_b; a.ot[s] = out[s]->stride_t; a.oh[s] = out[s]->stride_h;
         a.heads[s] = in[s]->heads;
         a.w[s] = w[s];
+        wide = wide && aligned16(in[s]) && aligned16(out[s]) && reinterpret_cast<uintptr_t>(w[s]) % 16 == 0;
     }
     a.w_f32 = w_dtype == HQMQ_F32;
     a.T = T;
@@ -116,9 +307,8 @@ extern "C" int hqmq_launch_norm_rope(const hqmq_head_view *q, const hqmq_head_vi
     a.eps = eps;
     a.pos = pos;
     a.inv_freq = inv_freq;
-    const unsigned n = (unsigned)((int64_t)B * T);
-    const cudaError_t e = dtype == HQMQ_BF16
-        ? launch_pdl(k_norm_rope<__nv_bfloat16>, dim3(n), dim3(NR_WARPS * 32), 0, stream, a)
-        : launch_pdl(k_norm_rope<float>, dim3(n), dim3(NR_WARPS * 32), 0, stream, a);
+    const unsigned tokens = (unsigned)((int64_t)B * T);
+    const cudaError_t e = dtype == HQMQ_BF16 ? launch_norm_rope<__nv_bfloat16>(a, tokens, wide, stream)
+                                             : launch_norm_rope<float>(a, tokens, wide, stream);
     return e == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }

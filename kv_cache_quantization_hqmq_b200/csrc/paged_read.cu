@@ -1,63 +1,171 @@
 // paged_read.cu -- the dense K or V of a paged cache's tokens
 // (include/hqmq.h, hqmq_paged_read).
+//
+// A CTA takes up to 256 tokens of one sequence and head: the head's codewords
+// go to shared memory, the tokens' flag words become slots (a scan that starts
+// anew with every page), then each warp decodes its tokens, a lane two chunks
+// (bf16) or one (fp32), so that every store is 16 bytes and a token's row is
+// contiguous.  The loads of several steps are issued before the first is used.
 #include "paged.cuh"
 
 namespace hqmq {
 
 constexpr int PR_WARPS = 8;
+constexpr int PR_THREADS = PR_WARPS * 32;
+constexpr int PR_COPIES = 4;                  // of the codeword table: bank conflicts in pairs only
 
 struct ReadArgs {
     PagesDev p;
     const int *len, *table;
-    int max_pages, T;
+    int max_pages, T, span;                   // span: tokens of a CTA, 32 .. 256
     void *y;
     DevStatus *st;
 };
 
-__device__ __forceinline__ void store_chunk(float *y, float4 v) {
-    *reinterpret_cast<float4 *>(y) = v;
-}
-__device__ __forceinline__ void store_chunk(__nv_bfloat16 *y, float4 v) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2 *>(y) = make_uint2(*reinterpret_cast<uint32_t *>(&a),
-                                               *reinterpret_cast<uint32_t *>(&b));
+struct ReadTok {
+    long long page;                           // page * heads + head, < 0: leave the row
+    uint32_t flags;
+    int slot;
+};
+
+__device__ __forceinline__ float4 half4(uint2 h) {
+    return make_float4(f16_bits_to_f32(h.x & 0xFFFFu), f16_bits_to_f32(h.x >> 16), f16_bits_to_f32(h.y & 0xFFFFu),
+                       f16_bits_to_f32(h.y >> 16));
 }
 
-// A warp takes one token of one head, a lane one chunk.
-template <typename E> __global__ void __launch_bounds__(PR_WARPS * 32) k_paged_read(ReadArgs a) {
+// CPL: chunks a lane takes (2: bf16, 1: fp32); a warp's step covers CPL tokens.
+template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(ReadArgs a) {
+    extern __shared__ float4 s_tab[];         // [24 S + 1][PR_COPIES]
+    __shared__ ReadTok s_tok[PR_THREADS];
+    __shared__ uint32_t s_sum[PR_WARPS];
     pdl_wait();
+    pdl_trigger();
     const PagesDev &p = a.p;
-    const int lane = threadIdx.x & 31;
-    const int head = blockIdx.y, seq = blockIdx.z;
-    const int t = blockIdx.x * PR_WARPS + (threadIdx.x >> 5);
-    if (t >= min(a.len[seq], a.T)) return;
-    const int col = t >> p.page_shift, row = t & (p.page_size - 1);
-    const int page = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
-    if (page < 0 || page >= p.n_pages) {
-        if (lane == 0 && a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
-        return;
-    }
-    const size_t at = p.at(page, head, row);
-    const uint32_t idx = token_index(p.words + at * p.b, p.b, lane);
-    const float r = f16_bits_to_f32(p.radius[at * PG_CHUNKS + lane]);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (idx < 24u * p.S) {
-        const float4 c = codeword((int)(idx % 24u), __ldg(p.cb + (size_t)head * p.S + idx / 24u));
-        v = make_float4(__fmul_rn(r, c.x), __fmul_rn(r, c.y), __fmul_rn(r, c.z), __fmul_rn(r, c.w));
-    } else if (a.st) {
-        atomicOr(&a.st->flags, HQMQ_FLAG_BAD_INDEX);
-    }
-    if (p.flags) {
-        const uint32_t f = p.flags[at];
-        const uint32_t slot = flags_before(p.flags + at - row, row, lane) + __popc(f & ((1u << lane) - 1u));
-        if (((f >> lane) & 1u) && slot < (uint32_t)p.cap) {
-            const uint2 h = p.slots(page, head)[slot];
-            v = make_float4(f16_bits_to_f32(h.x & 0xFFFFu), f16_bits_to_f32(h.x >> 16),
-                            f16_bits_to_f32(h.y & 0xFFFFu), f16_bits_to_f32(h.y >> 16));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = blockIdx.y, seq = blockIdx.z, t0 = blockIdx.x * a.span;
+    const int n = min(min(a.len[seq], a.T) - t0, a.span);
+    if (n <= 0) return;
+
+    // this thread's token: its page, flags and the slot of its first value
+    const int me = t0 + threadIdx.x;
+    ReadTok tok = {-1, 0u, 0};
+    int page = -1;
+    if ((int)threadIdx.x < n) {
+        const int col = me >> p.page_shift;
+        page = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
+        if (page < 0 || page >= p.n_pages) {
+            page = -1;
+            if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
+        } else {
+            tok.page = (long long)page * p.heads + head;
         }
     }
-    E *y = reinterpret_cast<E *>(a.y) + (((size_t)seq * p.heads + head) * a.T + t) * 128 + 4 * lane;
-    store_chunk(y, v);
+    const int row = me & (p.page_size - 1);
+    if (p.flags) {
+        uint32_t before = 0;                  // flagged chunks in the rows of the first page before t0
+        if (page >= 0) tok.flags = p.flags[p.at(page, head, row)];
+        const int row0 = t0 & (p.page_size - 1);
+        if (row0 > 0) {
+            const int col = t0 >> p.page_shift;
+            const int pg = col < a.max_pages ? a.table[(size_t)seq * a.max_pages + col] : -1;
+            if (pg >= 0 && pg < p.n_pages) before = flags_before(p.flags + p.at(pg, head, 0), row0, lane);
+        }
+        const uint32_t c = __popc(tok.flags);
+        uint32_t inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) s_sum[warp] = inc;
+        // sums of the page's earlier rows: within the warp, then of the warps between
+        uint32_t start = inc - c;
+        const int first = (int)threadIdx.x - row;          // the thread of the page's row 0 (< 0: before t0)
+        const int from = max(first, warp * 32) - warp * 32;  // its lane, if it is in this warp
+        start -= __shfl_sync(FULL, inc - c, from & 31);
+        __syncthreads();
+        for (int w = max(first, 0) >> 5; w < warp; ++w) start += s_sum[w];
+        if (first < 0) start += before;
+        tok.slot = (int)start;
+    }
+    s_tok[threadIdx.x] = tok;
+    const uint32_t words = 24u * p.S;
+    for (uint32_t e = threadIdx.x; e <= words; e += PR_THREADS) {
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < words) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
+#pragma unroll
+        for (int r = 0; r < PR_COPIES; ++r) s_tab[e * PR_COPIES + ((r + e) & (PR_COPIES - 1))] = c;
+    }
+    __syncthreads();
+
+    constexpr int STEPS = 4;                  // loads in flight: STEPS tokens a lane
+    const int sub = CPL == 2 ? lane >> 4 : 0, c0 = CPL == 2 ? 2 * (lane & 15) : lane;
+    const uint32_t bit = (uint32_t)c0 * p.b, wi = bit >> 5, sh = bit & 31u, mask = (1u << p.b) - 1u;
+    const float4 *tab = s_tab + (lane & (PR_COPIES - 1));
+    bool bad = false;
+    for (int i0 = warp * STEPS * CPL; i0 < n; i0 += PR_WARPS * STEPS * CPL) {
+        uint32_t lo[STEPS], hi[STEPS], rad[STEPS];
+        uint2 val[STEPS];
+        ReadTok k[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int i = i0 + s * CPL + sub;
+            k[s].page = -1;
+            if (i < n) k[s] = s_tok[i];
+            lo[s] = hi[s] = rad[s] = 0u;
+            if (k[s].page < 0) continue;
+            const size_t at = ((size_t)k[s].page << p.page_shift) + ((t0 + i) & (p.page_size - 1));
+            const uint32_t *w = p.words + at * p.b;
+            lo[s] = __ldcs(w + wi);
+            hi[s] = wi + 1 < p.b ? __ldcs(w + wi + 1) : 0u;
+            if (CPL == 2) rad[s] = __ldcs(reinterpret_cast<const uint32_t *>(p.radius + at * PG_CHUNKS) + (lane & 15));
+            else rad[s] = p.radius[at * PG_CHUNKS + lane];
+            k[s].slot += __popc(k[s].flags & ((1u << c0) - 1u));
+            k[s].flags = (k[s].flags >> c0) & (CPL == 2 ? 3u : 1u);
+            if (k[s].flags && k[s].slot < p.cap)
+                val[s] = __ldcs(reinterpret_cast<const uint2 *>(p.val) + (size_t)k[s].page * p.cap + k[s].slot);
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (k[s].page < 0) continue;
+            const int i = i0 + s * CPL + sub;
+            // CPL b bits: one or two words (b <= 11)
+            const uint32_t v = __funnelshift_r(lo[s], hi[s], sh);
+            float4 y[CPL];
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                const uint32_t idx = (v >> (c * p.b)) & mask;
+                const float r = f16_bits_to_f32(c ? rad[s] >> 16 : rad[s] & 0xFFFFu);
+                const float4 w = tab[min(idx, words) * PR_COPIES];
+                y[c] = make_float4(__fmul_rn(r, w.x), __fmul_rn(r, w.y), __fmul_rn(r, w.z), __fmul_rn(r, w.w));
+                if (idx >= words) {           // (not r 0: r may be infinite)
+                    y[c] = w;
+                    bad = true;
+                }
+            }
+            if (k[s].flags && k[s].slot < p.cap) {
+                y[CPL == 2 && !(k[s].flags & 1u) ? CPL - 1 : 0] = half4(val[s]);
+                if (CPL == 2 && k[s].flags == 3u && k[s].slot + 1 < p.cap)
+                    y[CPL - 1] = half4(__ldcs(reinterpret_cast<const uint2 *>(p.val) + (size_t)k[s].page * p.cap +
+                                              k[s].slot + 1));
+            }
+            const size_t out = (((size_t)seq * p.heads + head) * a.T + t0 + i) * 128 + 4 * c0;
+            if (CPL == 2) {
+                uint32_t h[4];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    const __nv_bfloat162 p0 = __floats2bfloat162_rn(y[c].x, y[c].y),
+                                         p1 = __floats2bfloat162_rn(y[c].z, y[c].w);
+                    h[2 * c] = *reinterpret_cast<const uint32_t *>(&p0);
+                    h[2 * c + 1] = *reinterpret_cast<const uint32_t *>(&p1);
+                }
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.y) + out) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.y) + out) = y[0];
+            }
+        }
+    }
+    if (bad && a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_INDEX);
 }
 
 }  // namespace hqmq
@@ -74,9 +182,15 @@ extern "C" int hqmq_launch_paged_read(const hqmq_kv_pages *c, uint32_t b, int n_
     a.T = T;
     a.y = y;
     a.st = reinterpret_cast<DevStatus *>(st);
-    const dim3 grid((unsigned)((T + PR_WARPS - 1) / PR_WARPS), (unsigned)c->heads, (unsigned)n_seqs);
-    const cudaError_t e = out_dtype == HQMQ_BF16
-        ? launch_pdl(k_paged_read<__nv_bfloat16>, grid, dim3(PR_WARPS * 32), 0, stream, a)
-        : launch_pdl(k_paged_read<float>, grid, dim3(PR_WARPS * 32), 0, stream, a);
-    return e == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
+    // 256 tokens a CTA (its codeword table then costs a tenth of the work), fewer where that would leave
+    // SMs idle
+    a.span = 256;
+    while (a.span > 32 && (int64_t)((T + a.span - 1) / a.span) * c->heads * n_seqs < 2 * 148) a.span /= 2;
+    const size_t smem = (size_t)(24 * c->S + 1) * PR_COPIES * sizeof(float4);
+    auto kern = out_dtype == HQMQ_BF16 ? k_paged_read<2> : k_paged_read<1>;
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return HQMQ_ERR_CUDA;
+    const dim3 grid((unsigned)((T + a.span - 1) / a.span), (unsigned)c->heads, (unsigned)n_seqs);
+    return launch_pdl(kern, grid, dim3(PR_THREADS), smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }
