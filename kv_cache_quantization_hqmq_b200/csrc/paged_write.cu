@@ -9,25 +9,25 @@
 //
 // The index is the argmax of the exact scores <x, q_p q_s>: fp32 scores decide
 // unless the two best lie within rounding of each other; then fp64 does.
-//   * k_paged_write<SEARCH = 1> (prefill): the search table of the head names
-//     up to 8 candidates per chunk; their codewords sit in shared memory.  A
-//     warp keeps four tokens' table records in flight.
-//   * k_paged_write<SEARCH = 0> (decode steps, and heads without tables): the
-//     loop over the S secondary codewords, y = x conj(q_s) scoring the 24
-//     primaries at once.  A run of few tokens shares each token's loop among
-//     the CTA's warps.
+//   * k_paged_write_table (prefill): the search table of the head names up to 8
+//     candidates per chunk; their codewords sit in shared memory.  A warp keeps
+//     eight tokens and four tokens' table records in flight.
+//   * k_paged_write_loop (decode steps, small codebooks, heads without
+//     tables): the loop over the S secondary codewords, y = x conj(q_s)
+//     scoring the 24 primaries at once.  A run of one or two tokens shares each
+//     token's loop among the CTA's warps.
 #include "paged.cuh"
 
 #include "search.cuh"
 
 namespace hqmq {
 
-constexpr int PW_WARPS = 8;
-constexpr int PW_THREADS = PW_WARPS * 32;
-constexpr int PW_MAX_PAGE = 256;
+constexpr int PW_LOOP_WARPS = 4, PW_TABLE_WARPS = 8;
+constexpr int PW_TOKENS = 8;                  // tokens a warp of the table kernel holds
 constexpr int PW_COPIES = 4;                  // of the codeword table
-constexpr int PW_BATCH = 4;                   // tokens a warp searches at once
+constexpr int PW_BATCH = 4;                   // of them, tokens whose records are in flight
 constexpr int PW_SEARCH_FROM = 8;             // tokens of a sequence, on average
+constexpr uint32_t PW_SEARCH_S = 12;
 
 struct WriteArgs {
     PagesDev p[2];
@@ -151,6 +151,24 @@ __device__ __forceinline__ Best scan_secondaries(float x0, float x1, float x2, f
     }
     return b;
 }
+// The 2T element of the best score of y, or -1 where fp32 cannot tell: the two families, the two largest
+// axes or the sign of a half unit's component within rounding.
+__device__ __forceinline__ int closest_clear(float y0, float y1, float y2, float y3) {
+    const float a0 = fabsf(y0), a1 = fabsf(y1), a2 = fabsf(y2), a3 = fabsf(y3);
+    const float h0 = fmaxf(a0, a1), l0 = fminf(a0, a1), h1 = fmaxf(a2, a3), l1 = fminf(a2, a3);
+    const float m = fmaxf(h0, h1), next = fmaxf(fminf(h0, h1), h0 >= h1 ? l0 : l1);
+    const float sum = (a0 + a1) + (a2 + a3), axis = m + m, near = 4e-6f * fmaxf(axis, sum);
+    if (fabsf(axis - sum) <= near) return -1;
+    if (axis > sum) {
+        if (2.0f * (m - next) <= near) return -1;
+        const int ax = a0 == m ? 0 : a1 == m ? 1 : a2 == m ? 2 : 3;
+        const float y = ax == 0 ? y0 : ax == 1 ? y1 : ax == 2 ? y2 : y3;
+        return 2 * ax + (y < 0.0f ? 1 : 0);
+    }
+    if (fminf(l0, l1) <= near) return -1;
+    return 8 + (y0 < 0.0f ? 1 : 0) + (y1 < 0.0f ? 2 : 0) + (y2 < 0.0f ? 4 : 0) + (y3 < 0.0f ? 8 : 0);
+}
+
 // The index, from the best of all S secondaries.
 __device__ __forceinline__ uint32_t settle_index(float x0, float x1, float x2, float x3, const float4 *s_cb,
                                                  uint32_t S, Best b) {
@@ -166,94 +184,159 @@ __device__ __forceinline__ uint32_t settle_index(float x0, float x1, float x2, f
             }
         }
     }
-    return b.s * 24u + (uint32_t)Score64(x0, x1, x2, x3, s_cb[b.s]).closest();
+    float y0, y1, y2, y3;
+    dot_conj_score2(x0, x1, x2, x3, s_cb[b.s], y0, y1, y2, y3);
+    int c = closest_clear(y0, y1, y2, y3);
+    if (c < 0) c = Score64(x0, x1, x2, x3, s_cb[b.s]).closest();
+    return b.s * 24u + (uint32_t)c;
 }
 
+// The largest r2 whose rounded root is not above th: r = RN(sqrt(r2)) > th exactly where r2 > this (the
+// root is monotone).  th NaN or infinite: nothing is above it.
+__device__ __forceinline__ float square_threshold(float th) {
+    if (!(th >= 0.f)) return th < 0.f ? -1.f : INFINITY;
+    float c = th * th;
+    while (__fsqrt_rn(c) > th) c = __uint_as_float(__float_as_uint(c) - 1u);
+    while (c < INFINITY && __fsqrt_rn(__uint_as_float(__float_as_uint(c) + 1u)) <= th) c = __uint_as_float(__float_as_uint(c) + 1u);
+    return c;
+}
+__device__ __forceinline__ float square_norm(float x0, float x1, float x2, float x3) {
+    return __fmaf_rn(x3, x3, __fmaf_rn(x2, x2, __fmaf_rn(x1, x1, __fmul_rn(x0, x0))));
+}
+
+// One coordinate's cell as the mantissa of 2^23 + cell: the map of search.cuh, shrunk by 2^-20 and moved
+// by 2^-17 so that t = +-1 (up to rounding) stay inside the grid, which moves a cell's border by 3.2e-6 at
+// most; cells list what can win up to 1e-5 beyond their borders.
+__device__ __forceinline__ uint32_t cell_bits(float t) {
+    constexpr float HG = 0.5f * LUT_G, SHRINK = 1.0f - 1.0f / 1048576.0f;
+    const float v = fmaf(t, fmaf(MAP_B * HG * SHRINK, t * t, MAP_A * HG * SHRINK), HG + 1.0f / 131072.0f);
+    return __float_as_uint(__fadd_rz(v, 8388608.0f));
+}
 // The table record of a chunk (finite, not 0): search.cuh.
-__device__ __forceinline__ const uint4 *record_of(const uint4 *tb, float x0, float x1, float x2, float x3) {
+__device__ __forceinline__ uint32_t record_of(float x0, float x1, float x2, float x3) {
     const float a0 = fabsf(x0), a1 = fabsf(x1), a2 = fabsf(x2), a3 = fabsf(x3);
     const float m = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
     const bool e0 = a0 == m, e01 = e0 || a1 == m, e012 = e01 || a2 == m;
-    const int ax = e0 ? 0 : e01 ? 1 : e012 ? 2 : 3;
+    const uint32_t ax = e0 ? 0u : e01 ? 2u : e012 ? 4u : 6u;
     const float xa = e0 ? x0 : e01 ? x1 : e012 ? x2 : x3;
     const float c1 = e0 ? x1 : x0, c2 = e01 ? x2 : x1, c3 = e012 ? x3 : x2;
-    const float inv = __fdividef(1.0f, m);    // (cells are widened by far more than its error)
-    const int cell = (cell_coord(c1 * inv) * LUT_G + cell_coord(c2 * inv)) * LUT_G + cell_coord(c3 * inv);
-    return tb + (2 * ax + (xa < 0.0f ? 1 : 0)) * LUT_CELLS + cell;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(m));
+    constexpr uint32_t BASE = 0x4B000000u * (LUT_G * LUT_G + LUT_G + 1u);
+    const uint32_t cell = cell_bits(c1 * inv) * (LUT_G * LUT_G) + cell_bits(c2 * inv) * LUT_G + cell_bits(c3 * inv) - BASE;
+    return (ax + (__float_as_uint(xa) >> 31)) * LUT_CELLS + cell;
 }
 
-__device__ __forceinline__ double exact_score(float x0, float x1, float x2, float x3, uint32_t id, const float4 *s_cb) {
-    const float4 q = s_cb[id / 24u];
-    float p0, p1, p2, p3;
-    element_2t((int)(id % 24u), p0, p1, p2, p3);
-    const double a = p0, b = p1, c = p2, d = p3, w = q.x, i = q.y, j = q.z, k = q.w;
-    return x0 * (a * w - b * i - c * j - d * k) + x1 * (a * i + b * w + c * k - d * j) +
-           x2 * (a * j - b * k + c * w + d * i) + x3 * (a * k + b * j - c * i + d * w);
-}
+// One token of a warp, a lane one chunk.
+struct Token {
+    float x0, x1, x2, x3;
+    bool search;                              // an index has to be found (else it is 0)
+};
 
-// The index among the record's candidates (kmax: the longest list of the warp).
-__device__ __forceinline__ uint32_t pick_candidate(float x0, float x1, float x2, float x3, uint4 rec, uint32_t kmax,
-                                                   const float4 *tab, const float4 *s_cb) {
+// The index among the record's candidates (kmax: the longest list of the warp), `clear` unless another
+// score is as near as rounding.  A score's bits, the last three replaced by 7 - slot, order scores and
+// then slots as integers (the best score is above 0); 128 units of 2^-23 or 2^-24, relative, are 7.6e-6 at
+// least: NEAR_TIE's 4e-6 and twice the 2^-20 that the replaced bits can be worth.
+__device__ __forceinline__ uint32_t pick_candidate(const Token &t, uint4 rec, uint32_t kmax, const float4 *tab,
+                                                   bool &clear) {
     const uint32_t sl[4] = {rec.x, rec.y, rec.z, rec.w};
-    float best = -INFINITY, second = -INFINITY;
-    uint32_t bid = 0;
+    int best = -1, second = -1;
 #pragma unroll
     for (int k = 0; k < LUT_SLOTS; ++k) {
         if ((uint32_t)k >= kmax) break;       // (warp-uniform)
         const uint32_t id = (sl[k >> 1] >> ((k & 1) * 16)) & LUT_ID_MASK;
         const float4 c = tab[id * PW_COPIES];
-        const float sc = fmaf(x3, c.w, fmaf(x2, c.z, fmaf(x1, c.y, x0 * c.x)));
-        second = fmaxf(second, fminf(sc, best));
-        if (sc > best) {
-            best = sc;
-            bid = id;
-        }
+        const float sc = fmaf(t.x3, c.w, fmaf(t.x2, c.z, fmaf(t.x1, c.y, t.x0 * c.x)));
+        const int key = (int)((__float_as_uint(sc) & ~7u) | (7u - k));
+        second = max(second, min(key, best));
+        best = max(best, key);
     }
-    if (second >= best * NEAR_TIE && best > 0.f) {            // (0: nothing to search)
-        double b64 = -1.0;
-        const uint32_t n = (rec.x >> 12) & 0xFu;
-        for (uint32_t k = 0; k < n; ++k) {
-            const uint32_t w = k < 2 ? sl[0] : k < 4 ? sl[1] : k < 6 ? sl[2] : sl[3];
-            const uint32_t id = (w >> ((k & 1u) * 16)) & LUT_ID_MASK;
-            const double e = exact_score(x0, x1, x2, x3, id, s_cb);
-            if (e > b64) {
-                b64 = e;
-                bid = id;
-            }
-        }
-    }
-    return bid;
+    const int k = 7 - (best & 7);
+    const uint32_t w = k < 4 ? (k < 2 ? sl[0] : sl[1]) : (k < 6 ? sl[2] : sl[3]);
+    const uint32_t id = (w >> ((k & 1) * 16)) & LUT_ID_MASK;
+    clear = !t.search || (best - second > 128 && (rec.x & 0xF000u) != 0u);
+    return t.search ? id : 0u;
 }
 
-// One token of a warp, a lane one chunk: flags, values and radius; what is
-// left to search (0 if nothing is).
-struct Token {
-    float x0, x1, x2, x3;
-    bool search;
-};
+// A stored token's index words again, by the loop over the codebook: for what the table's candidates in
+// fp32 could not tell, and for cells with more candidates than a record holds.  Out of line and after the
+// warp's other tokens, so that it costs them no registers.
+template <int DT, int BB>
+__device__ __noinline__ void settle_token(const PagesDev &p, const char *x, size_t at, const float4 *s_cb, int lane) {
+    RawChunk<DT> c;
+    c.load(x, lane);
+    Token t = {c.e(0), c.e(1), c.e(2), c.e(3), false};
+    if (p.flags && ((p.flags[at] >> lane) & 1u)) t.x0 = t.x1 = t.x2 = t.x3 = 0.f;
+    const float r = chunk_norm(t.x0, t.x1, t.x2, t.x3);
+    uint32_t idx = 0;
+    if (r > 0.f && r < INFINITY)
+        idx = settle_index(t.x0, t.x1, t.x2, t.x3, s_cb, p.S,
+                           scan_secondaries(t.x0, t.x1, t.x2, t.x3, s_cb, 0, p.S));
+    __syncwarp();
+    pack_group32<BB>(idx, p.b, lane, pack_const(p.b, lane), p.words + at * p.b);
+}
+
 struct Tally {
     unsigned out, over, sat, nf;
-};
-__device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t at, uint2 *slots, bool med3,
-                                            uint32_t mask, int slot0, int lane, Tally &n) {
-    if (med3) {
-        const int slot = slot0 + __popc(mask & ((1u << lane) - 1u));
-        const bool out = (mask >> lane) & 1u, kept = out && slot < p.cap;
-        const uint32_t f = __ballot_sync(FULL, kept);
-        if (lane == 0) p.flags[at] = f;
-        if (kept) {
-            int sv = 0;
-            const uint32_t h01 = f32x2_to_f16x2_sat(t.x0, t.x1, sv);
-            const uint32_t h23 = f32x2_to_f16x2_sat(t.x2, t.x3, sv);
-            n.sat += sv;
-            slots[slot] = make_uint2(h01, h23);
-            t.x0 = t.x1 = t.x2 = t.x3 = 0.f;
+    __device__ __forceinline__ void add_to(DevStatus *st, int lane) const {
+        if (!st) return;
+        const unsigned o = __reduce_add_sync(FULL, out), ov = __reduce_add_sync(FULL, over);
+        const unsigned sa = __reduce_add_sync(FULL, sat), f = __reduce_add_sync(FULL, nf);
+        if (lane == 0) {
+            if (o) atomicAdd(&st->n_outliers, (unsigned long long)o);
+            if (ov) atomicOr(&st->flags, HQMQ_FLAG_OUTLIER_OVERFLOW);
+            status_add(st, HQMQ_FLAG_SATURATED, &st->n_saturated, sa);
+            status_add(st, HQMQ_FLAG_NONFINITE, &st->n_nonfinite, f);
         }
-        n.out += out;
-        n.over += out && !kept;
+    }
+};
+
+// Where a run goes.
+struct Place {
+    size_t at0;                               // flat index of its first row
+    uint2 *slots;
+    const char *x;                            // its first token's chunks of this head
+};
+template <int DT>
+__device__ __forceinline__ bool find_place(const WriteArgs &a, const PagesDev &p, const Run &r, int head, int role,
+                                           Place &pl) {
+    int page = -1;
+    if (!r.bad && r.col < a.max_pages) page = a.table[(size_t)r.seq * a.max_pages + r.col];
+    if (page < 0 || page >= p.n_pages) {
+        if (threadIdx.x == 0 && a.st_out) atomicOr(&a.st_out->flags, HQMQ_FLAG_BAD_PAGE);
+        return false;
+    }
+    pl.at0 = p.at(page, head, r.row0);
+    pl.slots = p.slots(page, head);
+    pl.x = reinterpret_cast<const char *>(a.x[role]) +
+           (head * a.sh[role] + r.token0 * a.st[role]) * (int64_t)(DT == HQMQ_BF16 ? 2 : 4);
+    return true;
+}
+
+// Flags, values and radius of a token (mask: chunks above the threshold; slot0: the first one's slot).
+__device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t at, uint2 *slots, uint32_t mask,
+                                            int slot0, int lane, Tally &n) {
+    if (p.flags) {
+        uint32_t f = 0;
+        if (mask) {                           // (warp-uniform)
+            const int slot = slot0 + __popc(mask & ((1u << lane) - 1u));
+            const bool out = (mask >> lane) & 1u, kept = out && slot < p.cap;
+            f = __ballot_sync(FULL, kept);
+            if (kept) {
+                int sv = 0;
+                const uint32_t h01 = f32x2_to_f16x2_sat(t.x0, t.x1, sv);
+                const uint32_t h23 = f32x2_to_f16x2_sat(t.x2, t.x3, sv);
+                n.sat += sv;
+                slots[slot] = make_uint2(h01, h23);
+                t.x0 = t.x1 = t.x2 = t.x3 = 0.f;
+            }
+            n.out += out;
+            n.over += out && !kept;
+        }
+        if (lane == 0) p.flags[at] = f;
     }
     const float r = chunk_norm(t.x0, t.x1, t.x2, t.x3);
-    const bool finite = r == r && r != __int_as_float(0x7F800000);
+    const bool finite = r < INFINITY;         // (false for NaN)
     uint16_t rh = 0x7E00u;
     if (finite) {
         int sat = 0;
@@ -266,34 +349,30 @@ __device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t 
     p.radius[at * PG_CHUNKS + lane] = rh;
 }
 
-template <int DT, int SEARCH>
-__global__ void __launch_bounds__(PW_THREADS, SEARCH ? 3 : 5) k_paged_write(WriteArgs a) {
-    extern __shared__ float4 s_tab[];         // SEARCH: [24 S + 1][PW_COPIES] codewords
+template <int DT, int BB>
+__global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(const __grid_constant__ WriteArgs a) {
+    constexpr int WARPS = PW_TABLE_WARPS, THREADS = WARPS * 32, BLOCK = WARPS * PW_TOKENS;
+    extern __shared__ float4 s_tab[];         // [24 S + 1][PW_COPIES] codewords
     __shared__ Run s_run;
     __shared__ float4 s_cb[PG_MAX_S];
-    __shared__ uint32_t s_mask[PW_MAX_PAGE];  // outlier masks of the run's rows
-    __shared__ int s_slot[PW_MAX_PAGE];       // first slot of each row
-    __shared__ Best s_best[SEARCH ? 1 : PW_THREADS];
+    __shared__ uint32_t s_cnt[WARPS + 1];     // outliers of each warp's tokens, and before the block
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int head = blockIdx.y, role = blockIdx.z;
     const PagesDev &p = a.p[role];
     pdl_wait();
     pdl_trigger();
-    const bool med3 = p.flags != nullptr;
-    const float th = med3 ? p.thr[head] : 0.f;
-    for (uint32_t i = threadIdx.x; i < p.S; i += PW_THREADS) s_cb[i] = __ldg(p.cb + (size_t)head * p.S + i);
-    if (SEARCH) {
-        const uint32_t words = 24u * p.S;
-        for (uint32_t e = threadIdx.x; e <= words; e += PW_THREADS) {
-            float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e < words) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
+    const float th2 = p.flags ? square_threshold(p.thr[head]) : INFINITY;
+    const uint32_t words = 24u * p.S;
+    for (uint32_t i = threadIdx.x; i < p.S; i += THREADS) s_cb[i] = __ldg(p.cb + (size_t)head * p.S + i);
+    for (uint32_t e = threadIdx.x; e <= words; e += THREADS) {
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < words) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
 #pragma unroll
-            for (int r = 0; r < PW_COPIES; ++r) s_tab[e * PW_COPIES + ((r + e) & (PW_COPIES - 1))] = c;
-        }
+        for (int r = 0; r < PW_COPIES; ++r) s_tab[e * PW_COPIES + ((r + e) & (PW_COPIES - 1))] = c;
     }
-    const size_t esz = DT == HQMQ_BF16 ? 2 : 4;
-    const char *x = reinterpret_cast<const char *>(a.x[role]) + head * a.sh[role] * (int64_t)esz;
-    const int64_t xt = a.st[role] * (int64_t)esz;
+    const int64_t xt = a.st[role] * (int64_t)(DT == HQMQ_BF16 ? 2 : 4);
+    const uint4 *tb = p.table + (size_t)head * LUT_ENTRIES;
+    const float4 *tab = s_tab + (lane & (PW_COPIES - 1));
     const PackConst pc = pack_const(p.b, lane);
     Tally n = {0, 0, 0, 0};
 
@@ -305,131 +384,148 @@ __global__ void __launch_bounds__(PW_THREADS, SEARCH ? 3 : 5) k_paged_write(Writ
         __syncthreads();
         const Run r = s_run;
         if (r.n == 0) break;                  // (there are no more)
-        int page = -1;
-        if (!r.bad && r.col < a.max_pages) page = a.table[(size_t)r.seq * a.max_pages + r.col];
-        if (page < 0 || page >= p.n_pages) {
-            if (threadIdx.x == 0 && a.st_out) atomicOr(&a.st_out->flags, HQMQ_FLAG_BAD_PAGE);
-            __syncthreads();                  // (s_run)
-            continue;
-        }
-        const size_t at0 = p.at(page, head, r.row0);
-        uint2 *slots = p.slots(page, head);
-        const char *x0p = x + r.token0 * xt;
-        if (med3) {
-            for (int t = warp; t < r.n; t += PW_WARPS) {
-                float x0, x1, x2, x3;
-                load_chunk<DT>(x0p + t * xt, lane, x0, x1, x2, x3);
-                const uint32_t m = __ballot_sync(FULL, chunk_norm(x0, x1, x2, x3) > th);
-                if (lane == 0) s_mask[t] = m;
-            }
-            uint32_t before = 0;
-            if (warp == 0) before = flags_before(p.flags + at0 - r.row0, r.row0, lane);
-            __syncthreads();
-            if (warp == 0) {
-                int slot = (int)before;
-                for (int t0 = 0; t0 < r.n; t0 += 32) {
-                    const int t = t0 + lane;
-                    const int c = t < r.n ? __popc(s_mask[t]) : 0;
-                    int inc = c;
+        Place pl;
+        const bool there = find_place<DT>(a, p, r, head, role, pl);
+        // blocks of 64 tokens, 8 to a warp
+        for (int b0 = 0; there && b0 < r.n; b0 += BLOCK) {
+            const int t0 = b0 + warp * PW_TOKENS, mine = min(max(r.n - t0, 0), PW_TOKENS);
+            RawChunk<DT> x[PW_TOKENS];
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int u = __shfl_up_sync(FULL, inc, o);
-                        if (lane >= o) inc += u;
-                    }
-                    if (t < r.n) s_slot[t] = slot + inc - c;
-                    slot += __shfl_sync(FULL, inc, 31);
-                }
+            for (int i = 0; i < PW_TOKENS; ++i) {
+                x[i].zero();
+                if (i < mine) x[i].load(pl.x + (t0 + i) * xt, lane);
             }
-        }
-        __syncthreads();
-        if (SEARCH) {
-            const uint4 *tb = p.table + (size_t)head * LUT_ENTRIES;
-            for (int t0 = warp * PW_BATCH; t0 < r.n; t0 += PW_WARPS * PW_BATCH) {
+            uint32_t mask[PW_TOKENS] = {};
+            int slot = 0;
+            if (p.flags) {
+                int cnt = 0;
+#pragma unroll
+                for (int i = 0; i < PW_TOKENS; ++i) {
+                    mask[i] = __ballot_sync(FULL, square_norm(x[i].e(0), x[i].e(1), x[i].e(2), x[i].e(3)) > th2);
+                    if (i >= mine) mask[i] = 0u;              // (a threshold below 0 is passed by zeros)
+                    cnt += __popc(mask[i]);
+                }
+                if (lane == 0) s_cnt[warp] = cnt;
+                if (warp == 0) {              // (a later block: the rows before are this call's, counted in slots)
+                    const uint32_t f = b0 == 0 ? flags_before(p.flags + pl.at0 - r.row0, r.row0, lane) : s_cnt[WARPS];
+                    if (lane == 0) s_cnt[WARPS] = f;
+                }
+                __syncthreads();
+                slot = (int)s_cnt[WARPS];
+                for (int w = 0; w < warp; ++w) slot += (int)s_cnt[w];
+                uint32_t all = s_cnt[WARPS];
+                for (int w = 0; w < WARPS; ++w) all += s_cnt[w];
+                __syncthreads();
+                if (threadIdx.x == 0) s_cnt[WARPS] = all;
+            }
+            uint32_t unclear = 0;             // tokens of the warp
+#pragma unroll
+            for (int g = 0; g < PW_TOKENS; g += PW_BATCH) {
                 Token k[PW_BATCH];
                 uint4 rec[PW_BATCH];
 #pragma unroll
                 for (int i = 0; i < PW_BATCH; ++i) {
-                    k[i] = {0.f, 0.f, 0.f, 0.f, false};
-                    if (t0 + i < r.n) load_chunk<DT>(x0p + (t0 + i) * xt, lane, k[i].x0, k[i].x1, k[i].x2, k[i].x3);
-                }
-#pragma unroll
-                for (int i = 0; i < PW_BATCH; ++i) {
                     rec[i] = make_uint4(1u << 12, 0u, 0u, 0u);
-                    if (t0 + i >= r.n) continue;              // (warp-uniform)
-                    store_token(k[i], p, at0 + t0 + i, slots, med3, med3 ? s_mask[t0 + i] : 0u,
-                                med3 ? s_slot[t0 + i] : 0, lane, n);
-                    if (k[i].search) rec[i] = __ldg(record_of(tb, k[i].x0, k[i].x1, k[i].x2, k[i].x3));
+                    if (g + i >= mine) continue;              // (warp-uniform)
+                    const RawChunk<DT> &c = x[g + i];
+                    k[i] = {c.e(0), c.e(1), c.e(2), c.e(3), false};
+                    store_token(k[i], p, pl.at0 + t0 + g + i, pl.slots, mask[g + i], slot, lane, n);
+                    slot += __popc(mask[g + i]);
+                    if (k[i].search) rec[i] = __ldg(tb + record_of(k[i].x0, k[i].x1, k[i].x2, k[i].x3));
                 }
 #pragma unroll
                 for (int i = 0; i < PW_BATCH; ++i) {
-                    if (t0 + i >= r.n) continue;
+                    if (g + i >= mine) continue;
                     const uint32_t cnt = (rec[i].x >> 12) & 0xFu;
                     const uint32_t kmax = __reduce_max_sync(FULL, cnt);
-                    uint32_t idx = pick_candidate(k[i].x0, k[i].x1, k[i].x2, k[i].x3, rec[i], kmax,
-                                                  s_tab + (lane & (PW_COPIES - 1)), s_cb);
-                    if (!k[i].search) idx = 0;
-                    else if (cnt == 0)        // a cell with more candidates than a record holds
-                        idx = settle_index(k[i].x0, k[i].x1, k[i].x2, k[i].x3, s_cb, p.S,
-                                           scan_secondaries(k[i].x0, k[i].x1, k[i].x2, k[i].x3, s_cb, 0, p.S));
-                    __syncwarp();
-                    pack_group32<0>(idx, p.b, lane, pc, p.words + (at0 + t0 + i) * p.b);
+                    bool clear;
+                    const uint32_t idx = pick_candidate(k[i], rec[i], kmax, tab, clear);
+                    if (!__all_sync(FULL, clear)) unclear |= 1u << (g + i);
+                    pack_group32<BB>(idx, p.b, lane, pc, p.words + (pl.at0 + t0 + g + i) * p.b);
                 }
             }
-        } else {
-            // warps of a token: 8, 4, 2 or 1, each with a share of the secondaries
-            const int wpt = r.n == 1 ? 8 : r.n == 2 ? 4 : r.n <= 4 ? 2 : 1;
-            const int share = warp & (wpt - 1);
-            const uint32_t s0 = p.S * share / wpt, s1 = p.S * (share + 1) / wpt;
-            const int per = PW_WARPS / wpt;   // tokens at a time
-            for (int t0 = 0; t0 < r.n; t0 += per) {
-                const int t = t0 + warp / wpt;
-                Token k = {0.f, 0.f, 0.f, 0.f, false};
-                Best b = {-1.0f, -1.0f, 0};
-                if (t < r.n) {
-                    load_chunk<DT>(x0p + t * xt, lane, k.x0, k.x1, k.x2, k.x3);
-                    if (share == 0) {
-                        store_token(k, p, at0 + t, slots, med3, med3 ? s_mask[t] : 0u, med3 ? s_slot[t] : 0, lane, n);
-                    } else if (med3) {
-                        const uint32_t m = s_mask[t];
-                        const int slot = s_slot[t] + __popc(m & ((1u << lane) - 1u));
-                        if (((m >> lane) & 1u) && slot < p.cap) k.x0 = k.x1 = k.x2 = k.x3 = 0.f;
-                    }
-                    b = scan_secondaries(k.x0, k.x1, k.x2, k.x3, s_cb, s0, s1);
-                }
-                if (wpt > 1) {
-                    s_best[SEARCH ? 0 : threadIdx.x] = b;
-                    __syncthreads();
-                    if (share == 0) {
-                        for (int w = 1; w < wpt; ++w) {       // in order of s: the lowest of equal scores stays
-                            const Best o = s_best[SEARCH ? 0 : threadIdx.x + 32 * w];
-                            b.second = fmaxf(fmaxf(b.second, o.second), fminf(b.best, o.best));
-                            if (o.best > b.best) {
-                                b.best = o.best;
-                                b.s = o.s;
-                            }
-                        }
-                    }
-                }
-                if (share == 0 && t < r.n) {
-                    const uint32_t idx = k.search ? settle_index(k.x0, k.x1, k.x2, k.x3, s_cb, p.S, b) : 0u;
-                    __syncwarp();
-                    pack_group32<0>(idx, p.b, lane, pc, p.words + (at0 + t) * p.b);
-                }
-                if (wpt > 1) __syncthreads(); // (s_best)
+            __syncwarp();
+            for (; unclear; unclear &= unclear - 1u) {
+                const int i = __ffs(unclear) - 1;
+                settle_token<DT, BB>(p, pl.x + (t0 + i) * xt, pl.at0 + t0 + i, s_cb, lane);
             }
         }
-        __syncthreads();                      // (s_run, s_mask, s_slot)
+        __syncthreads();                      // (s_run, s_cnt)
     }
-    if (a.st_out) {
-        const unsigned o = __reduce_add_sync(FULL, n.out), ov = __reduce_add_sync(FULL, n.over);
-        const unsigned sa = __reduce_add_sync(FULL, n.sat), nf = __reduce_add_sync(FULL, n.nf);
-        if (lane == 0) {
-            if (o) atomicAdd(&a.st_out->n_outliers, (unsigned long long)o);
-            if (ov) atomicOr(&a.st_out->flags, HQMQ_FLAG_OUTLIER_OVERFLOW);
-            status_add(a.st_out, HQMQ_FLAG_SATURATED, &a.st_out->n_saturated, sa);
-            status_add(a.st_out, HQMQ_FLAG_NONFINITE, &a.st_out->n_nonfinite, nf);
+    n.add_to(a.st_out, lane);
+}
+
+template <int DT, int BB>
+__global__ void __launch_bounds__(PW_LOOP_WARPS * 32, 8) k_paged_write_loop(const __grid_constant__ WriteArgs a) {
+    constexpr int WARPS = PW_LOOP_WARPS, THREADS = WARPS * 32;
+    __shared__ float4 s_cb[PG_MAX_S];
+    __shared__ uint32_t s_cnt[WARPS];
+    __shared__ Best s_best[THREADS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = blockIdx.y, role = blockIdx.z;
+    const PagesDev &p = a.p[role];
+    pdl_wait();
+    pdl_trigger();
+    // (every warp finds the run by itself: no one waits for another)
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (threadIdx.x < p.S) q = __ldg(p.cb + (size_t)head * p.S + threadIdx.x);
+    const float thr = p.flags ? __ldg(p.thr + head) : 0.f;
+    const Run r = find_run(a, blockIdx.x, lane);
+    if (r.n == 0) return;
+    Place pl;
+    if (!find_place<DT>(a, p, r, head, role, pl)) return;
+    const int64_t xt = a.st[role] * (int64_t)(DT == HQMQ_BF16 ? 2 : 4);
+    // warps of a token: 4, 2 or 1, each with a share of the secondaries
+    const int wpt = r.n == 1 ? 4 : r.n == 2 ? 2 : 1, per = WARPS / wpt;
+    const int share = warp & (wpt - 1), own = warp / wpt;
+    RawChunk<DT> next;
+    next.zero();
+    if (own < r.n) next.load(pl.x + own * xt, lane);
+    uint32_t before = 0;                      // flagged chunks before the tokens of this round
+    if (p.flags) before = flags_before(p.flags + pl.at0 - r.row0, r.row0, lane);
+    if (threadIdx.x < p.S) s_cb[threadIdx.x] = q;
+    const float th2 = p.flags ? square_threshold(thr) : INFINITY;
+    const uint32_t s0 = p.S * share / wpt, s1 = p.S * (share + 1) / wpt;
+    const PackConst pc = pack_const(p.b, lane);
+    Tally n = {0, 0, 0, 0};
+    for (int t0 = 0; t0 < r.n; t0 += per) {
+        const int t = t0 + own;
+        const RawChunk<DT> c = next;
+        if (t + per < r.n) next.load(pl.x + (t + per) * xt, lane);
+        Token k = {c.e(0), c.e(1), c.e(2), c.e(3), false};
+        uint32_t mask = 0;
+        if (p.flags && t < r.n) mask = __ballot_sync(FULL, square_norm(k.x0, k.x1, k.x2, k.x3) > th2);
+        if (lane == 0) s_cnt[warp] = __popc(mask);
+        __syncthreads();
+        int slot = (int)before;
+        for (int w = 0; w < own; ++w) slot += (int)s_cnt[w * wpt];
+        for (int w = 0; w < per; ++w) before += s_cnt[w * wpt];
+        if (t < r.n) {
+            if (share == 0) {
+                store_token(k, p, pl.at0 + t, pl.slots, mask, slot, lane, n);
+            } else if (((mask >> lane) & 1u) && slot + __popc(mask & ((1u << lane) - 1u)) < p.cap) {
+                k.x0 = k.x1 = k.x2 = k.x3 = 0.f;
+            }
+        }
+        Best b = {-1.0f, -1.0f, 0};
+        if (t < r.n) b = scan_secondaries(k.x0, k.x1, k.x2, k.x3, s_cb, s0, s1);
+        if (share) s_best[threadIdx.x] = b;
+        __syncthreads();
+        if (share == 0 && t < r.n) {
+            for (int w = 1; w < wpt; ++w) {   // in order of s: the lowest of equal scores stays
+                const Best o = s_best[threadIdx.x + 32 * w];
+                b.second = fmaxf(fmaxf(b.second, o.second), fminf(b.best, o.best));
+                if (o.best > b.best) {
+                    b.best = o.best;
+                    b.s = o.s;
+                }
+            }
+            const uint32_t idx = k.search ? settle_index(k.x0, k.x1, k.x2, k.x3, s_cb, p.S, b) : 0u;
+            __syncwarp();
+            pack_group32<BB>(idx, p.b, lane, pc, p.words + (pl.at0 + t) * p.b);
         }
     }
+    n.add_to(a.st_out, lane);
 }
 
 }  // namespace hqmq
@@ -464,21 +560,27 @@ extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pag
     if (runs > n_tokens) runs = n_tokens;
     a.runs = (int)runs;
     const int roles = v ? 2 : 1;
-    // the tables pay from runs of a few tokens on (their codewords have to be brought to shared memory)
-    const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs;
     const uint32_t S = v && v->S > k->S ? v->S : k->S;
+    // the tables pay for runs of some tokens (their codewords have to be brought to shared memory) and
+    // codebooks of some size (the loop costs about 25 instructions a secondary, the table 250 in all)
+    const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs && S >= PW_SEARCH_S;
     const size_t smem = search ? (size_t)(24 * S + 1) * PW_COPIES * sizeof(float4) : 0;
-    // with tables a CTA goes through several runs of its head; 3 CTAs to an SM
-    int64_t gx = runs;
-    if (search) {
-        const int64_t fill = (3 * 148 + k->heads * roles - 1) / (k->heads * roles);
-        if (gx > fill) gx = fill;
-    }
+    // with tables a CTA goes through runs of 64 tokens or more
+    const int64_t gx = search && k->page_size < 64 ? (runs * k->page_size + 63) / 64 : runs;
     const dim3 grid((unsigned)gx, (unsigned)k->heads, (unsigned)roles);
-    auto kern = dtype == HQMQ_BF16 ? (search ? k_paged_write<HQMQ_BF16, 1> : k_paged_write<HQMQ_BF16, 0>)
-                                   : (search ? k_paged_write<HQMQ_F32, 1> : k_paged_write<HQMQ_F32, 0>);
+    const uint32_t bb = v && bv != bk ? 0 : bk;
+    auto kern = dtype == HQMQ_BF16
+        ? (search ? (bb == 8 ? k_paged_write_table<HQMQ_BF16, 8> : bb == 10 ? k_paged_write_table<HQMQ_BF16, 10>
+                                                                            : k_paged_write_table<HQMQ_BF16, 0>)
+                  : (bb == 8 ? k_paged_write_loop<HQMQ_BF16, 8> : bb == 10 ? k_paged_write_loop<HQMQ_BF16, 10>
+                                                                           : k_paged_write_loop<HQMQ_BF16, 0>))
+        : (search ? (bb == 8 ? k_paged_write_table<HQMQ_F32, 8> : bb == 10 ? k_paged_write_table<HQMQ_F32, 10>
+                                                                           : k_paged_write_table<HQMQ_F32, 0>)
+                  : (bb == 8 ? k_paged_write_loop<HQMQ_F32, 8> : bb == 10 ? k_paged_write_loop<HQMQ_F32, 10>
+                                                                          : k_paged_write_loop<HQMQ_F32, 0>));
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
-    return launch_pdl(kern, grid, dim3(PW_THREADS), smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
+    const dim3 block((search ? PW_TABLE_WARPS : PW_LOOP_WARPS) * 32);
+    return launch_pdl(kern, grid, block, smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }

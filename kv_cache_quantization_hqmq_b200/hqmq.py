@@ -401,26 +401,48 @@ def alloc_attention_ws(B, Hk, device="cuda"):
 
 
 # ---------------------------------------------------------------- paged cache
+_BF16, _F32, _I32, _F64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
+_DTYPE_CODE = {torch.bfloat16: HQMQ_BF16, torch.float32: HQMQ_F32}
+
+
 def _here(*tensors):
-    """The tensors are on the current CUDA device (the calls launch there)."""
+    """The current CUDA device, on which all of the tensors have to be (the calls launch there)."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:       # (-1 for a CPU tensor)
             raise ValueError("tensors must be on the current CUDA device %d, got one on %s "
                              "(call under torch.cuda.device)" % (dev, t.device))
+    return dev
+
+
+def _on(stream, dev):
+    """The stream's handle; None: torch's current stream of the device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _code(t):
+    c = _DTYPE_CODE.get(t.dtype)
+    return _dtype_code(t) if c is None else c
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _ints(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s, got %s %s"
                          % (name, shape, t.dtype, tuple(t.shape)))
 
 
 def _table(t, n_seqs, name="block_table"):
-    if t.dim() != 2 or t.shape[0] != n_seqs:
-        raise ValueError("%s must be [%d, max_pages], got %s" % (name, n_seqs, tuple(t.shape)))
-    _ints(name, t, tuple(t.shape))
-    return t.shape[1]
+    s = t.shape
+    if len(s) != 2 or s[0] != n_seqs or t.dtype is not _I32 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 [%d, max_pages], got %s %s"
+                         % (name, n_seqs, t.dtype, tuple(s)))
+    return s[1]
 
 
 class KVPages(ctypes.Structure):
@@ -479,18 +501,27 @@ def kv_pages(idx_words, radius, codebook, flags=None, out_val=None, thr=None, ta
     c = KVPages(_ptr(idx_words), _ptr(radius), _ptr(flags), _ptr(out_val), _ptr(codebook), _ptr(thr),
                 _ptr(table), S, n_pages, P, heads, cap)
     c._keep = (idx_words, radius, flags, out_val, codebook, thr, table)
+    c._ref = ctypes.byref(c)
     return c
 
 
 class _HeadView(ctypes.Structure):
+    """hqmq_head_view."""
     _fields_ = [("data", _P), ("stride_b", _I64), ("stride_t", _I64), ("stride_h", _I64), ("heads", _I)]
 
 
-def _head_view(x):
+_HeadViews = _I64 * 20                                    # four of them, as hqmq_qk_norm_rope takes them
+_VIEW = ctypes.sizeof(_HeadView)
+assert _VIEW == 40
+_NO_VIEWS = (0,) * 10
+
+
+def _view_words(x):
     sb, st, sh, sd = x.stride()
-    if sd != 1 and x.shape[3] > 1:
+    s = x.shape
+    if sd != 1 and s[3] > 1:
         raise ValueError("the last dimension must be contiguous")
-    return _HeadView(x.data_ptr(), sb, st, sh, x.shape[2])
+    return x.data_ptr(), sb, st, sh, s[2]
 
 
 def rope_inv_freq(R, base=10000.0, device="cuda"):
@@ -508,37 +539,47 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
     if x is None or x.dim() != 4:
         raise ValueError("q and k are [B, T, heads, D]")
     B, T, _, D = x.shape
+    dt = x.dtype
+    views = []
     for t, t_out, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
         if t is None:
             if t_out is not None or w is not None:
                 raise ValueError("an output or weight without its input")
+            views += _NO_VIEWS
             continue
-        if t_out is None or t.dim() != 4 or t.shape[:2] != (B, T) or t.shape[3] != D or \
-                t_out.shape != t.shape or t.dtype != x.dtype or t_out.dtype != x.dtype:
+        s = t.shape
+        if t_out is None or len(s) != 4 or s[0] != B or s[1] != T or s[3] != D or t_out.shape != s or \
+                t.dtype is not dt or t_out.dtype is not dt:
             raise ValueError("q, k and their outputs must agree in B, T, D and dtype")
-        if w is not None and (tuple(w.shape) != (D,) or not w.is_contiguous()):
+        if w is not None and (w.shape != (D,) or not w.is_contiguous()):
             raise ValueError("weights are contiguous [D]")
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        views += _view_words(t)
+        views += _view_words(t_out)
+    w = q_weight if q_weight is not None else k_weight
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise ValueError("the weights must have one dtype")
     R = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not _F64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous fp64 vector")
         R = 2 * inv_freq.shape[0]
         _ints("pos", pos, (B, T))
-    w = q_weight if q_weight is not None else k_weight
-    _here(q, k, q_out, k_out, pos, inv_freq, q_weight, k_weight)
-    views = [None if t is None else ctypes.byref(_head_view(t)) for t in (q, q_out, k, k_out)]
-    _check("hqmq_qk_norm_rope", _lib.hqmq_qk_norm_rope(
-        *views, _dtype_code(x), B, T, D, _ptr(q_weight), _ptr(k_weight),
-        HQMQ_BF16 if w is None else _dtype_code(w), float(eps), _ptr(pos), _ptr(inv_freq), R,
-        1 if interleaved else 0, _stream(stream)))
+    dev = _here(q, k, q_out, k_out, pos, inv_freq, q_weight, k_weight)
+    v = _HeadViews(*views)
+    qr = (ctypes.byref(v), ctypes.byref(v, _VIEW)) if q is not None else (None, None)
+    kr = (ctypes.byref(v, 2 * _VIEW), ctypes.byref(v, 3 * _VIEW)) if k is not None else (None, None)
+    rc = _lib.hqmq_qk_norm_rope(
+        *qr, *kr, _code(x), B, T, D, _addr(q_weight), _addr(k_weight), HQMQ_BF16 if w is None else _code(w),
+        eps, _addr(pos), _addr(inv_freq), R, 1 if interleaved else 0, _on(stream, dev))
+    if rc:
+        _check("hqmq_qk_norm_rope", rc)
 
 
 def _new_tokens(x, heads):
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128 or x.stride(2) != 1:
+    s = x.shape
+    if len(s) != 3 or s[1] != heads or s[2] != 128 or x.stride(2) != 1:
         raise ValueError("new tokens are [n_tokens, %d, 128] with a contiguous last dimension, got "
-                         "%s" % (heads, tuple(x.shape)))
+                         "%s" % (heads, tuple(s)))
 
 
 def hqmq_paged_write(xk, xv, k, v, block_table, cu_tokens, pos0, status=None, stream=None):
@@ -548,22 +589,22 @@ def hqmq_paged_write(xk, xv, k, v, block_table, cu_tokens, pos0, status=None, st
     block_table: int32 [n_seqs, max_pages]; cu_tokens: int32 [n_seqs + 1]; pos0:
     int32 [n_seqs].  xv and v may be None."""
     _new_tokens(xk, k.heads)
-    vs = (0, 0)
+    ks, vs, v_ref, v_keep = xk.stride(), (0, 0), None, None
     if v is not None:
         _new_tokens(xv, v.heads)
-        if xv.shape != xk.shape or xv.dtype != xk.dtype:
+        if xv.shape != xk.shape or xv.dtype is not xk.dtype:
             raise ValueError("xk and xv must agree in shape and dtype")
-        vs = xv.stride()
+        vs, v_ref, v_keep = xv.stride(), v._ref, v._keep[0]
     n_seqs = pos0.shape[0] if pos0.dim() == 1 else -1
     _ints("pos0", pos0, (n_seqs,))
     _ints("cu_tokens", cu_tokens, (n_seqs + 1,))
     max_pages = _table(block_table, n_seqs)
-    _here(xk, xv, k._keep[0], None if v is None else v._keep[0], block_table, cu_tokens, pos0, status)
-    _check("hqmq_paged_write", _lib.hqmq_paged_write(
-        ctypes.byref(k), None if v is None else ctypes.byref(v), _ptr(xk),
-        None if v is None else _ptr(xv), _dtype_code(xk), xk.stride(0), xk.stride(1), vs[0], vs[1],
-        xk.shape[0], n_seqs, _ptr(cu_tokens), _ptr(pos0), _ptr(block_table), max_pages,
-        _ptr(status), _stream(stream)))
+    dev = _here(xk, xv, k._keep[0], v_keep, block_table, cu_tokens, pos0, status)
+    rc = _lib.hqmq_paged_write(
+        k._ref, v_ref, xk.data_ptr(), _addr(xv), _code(xk), ks[0], ks[1], vs[0], vs[1], xk.shape[0], n_seqs,
+        cu_tokens.data_ptr(), pos0.data_ptr(), block_table.data_ptr(), max_pages, _addr(status), _on(stream, dev))
+    if rc:
+        _check("hqmq_paged_write", rc)
 
 
 def hqmq_paged_read(c, block_table, seq_len, y, status=None, stream=None):
@@ -574,10 +615,11 @@ def hqmq_paged_read(c, block_table, seq_len, y, status=None, stream=None):
         raise ValueError("y must be [n_seqs, %d, T, 128]" % c.heads)
     _ints("seq_len", seq_len, (B,))
     max_pages = _table(block_table, B)
-    _here(c._keep[0], block_table, seq_len, y, status)
-    _check("hqmq_paged_read", _lib.hqmq_paged_read(
-        ctypes.byref(c), B, _ptr(seq_len), _ptr(block_table), max_pages, T, _ptr(y), _dtype_code(y),
-        _ptr(status), _stream(stream)))
+    dev = _here(c._keep[0], block_table, seq_len, y, status)
+    rc = _lib.hqmq_paged_read(c._ref, B, seq_len.data_ptr(), block_table.data_ptr(), max_pages, T, y.data_ptr(),
+                              _code(y), _addr(status), _on(stream, dev))
+    if rc:
+        _check("hqmq_paged_read", rc)
     return y
 
 
@@ -600,7 +642,7 @@ def hqmq_attention_paged(q, k, v, block_table, seq_len, o, ws, prefix_table=None
     and the seq_len[b] tokens of sequence b's row of block_table (None: the
     prefix alone).  q: bf16 [B, Hq, 128]; o: bf16 or fp32 [B, Hq, 128]; lse:
     fp32 [B, Hq] or None; scale defaults to 1/sqrt(128)."""
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    if q.dim() != 3 or q.dtype is not _BF16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [B, Hq, 128] tensor")
     B, Hq, D = q.shape
     if D != 128 or o.shape != q.shape or not o.is_contiguous():
@@ -613,16 +655,16 @@ def hqmq_attention_paged(q, k, v, block_table, seq_len, o, ws, prefix_table=None
         need = (prefix_len + k.page_size - 1) // k.page_size
         if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
             raise ValueError("prefix_table must hold the prefix's %d pages" % need)
-        _ints("prefix_table", prefix_table, tuple(prefix_table.shape))
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or
-                            not lse.is_contiguous()):
+        _ints("prefix_table", prefix_table, prefix_table.shape)
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [B, Hq] tensor")
-    _here(q, k._keep[0], v._keep[0], block_table, seq_len, o, ws, prefix_table, lse, status)
-    _check("hqmq_attention_paged", _lib.hqmq_attention_paged(
-        _ptr(q), ctypes.byref(k), ctypes.byref(v), B, Hq, _ptr(seq_len), _ptr(block_table), max_pages,
-        _ptr(prefix_table), int(prefix_len), D ** -0.5 if scale is None else float(scale), _ptr(o),
-        _dtype_code(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-        _stream(stream)))
+    dev = _here(q, k._keep[0], v._keep[0], block_table, seq_len, o, ws, prefix_table, lse, status)
+    rc = _lib.hqmq_attention_paged(
+        q.data_ptr(), k._ref, v._ref, B, Hq, _addr(seq_len), _addr(block_table), max_pages, _addr(prefix_table),
+        prefix_len, D ** -0.5 if scale is None else scale, o.data_ptr(), _code(o), _addr(lse), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _addr(status), _on(stream, dev))
+    if rc:
+        _check("hqmq_attention_paged", rc)
     return o
 
 
