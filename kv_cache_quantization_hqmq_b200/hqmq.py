@@ -42,6 +42,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -510,18 +511,16 @@ class _HeadView(ctypes.Structure):
     _fields_ = [("data", _P), ("stride_b", _I64), ("stride_t", _I64), ("stride_h", _I64), ("heads", _I)]
 
 
-_HeadViews = _I64 * 20                                    # four of them, as hqmq_qk_norm_rope takes them
-_VIEW = ctypes.sizeof(_HeadView)
-assert _VIEW == 40
-_NO_VIEWS = (0,) * 10
+_pack_view = struct.Struct("=4qi4x").pack                # its bytes
+assert ctypes.sizeof(_HeadView) == 40 == len(_pack_view(0, 0, 0, 0, 0))
 
 
-def _view_words(x):
+def _head_view(x):
     sb, st, sh, sd = x.stride()
     s = x.shape
     if sd != 1 and s[3] > 1:
         raise ValueError("the last dimension must be contiguous")
-    return x.data_ptr(), sb, st, sh, s[2]
+    return _pack_view(x.data_ptr(), sb, st, sh, s[2])
 
 
 def rope_inv_freq(R, base=10000.0, device="cuda"):
@@ -545,7 +544,7 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
         if t is None:
             if t_out is not None or w is not None:
                 raise ValueError("an output or weight without its input")
-            views += _NO_VIEWS
+            views += (None, None)
             continue
         s = t.shape
         if t_out is None or len(s) != 4 or s[0] != B or s[1] != T or s[3] != D or t_out.shape != s or \
@@ -553,8 +552,7 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
             raise ValueError("q, k and their outputs must agree in B, T, D and dtype")
         if w is not None and (w.shape != (D,) or not w.is_contiguous()):
             raise ValueError("weights are contiguous [D]")
-        views += _view_words(t)
-        views += _view_words(t_out)
+        views += (_head_view(t), _head_view(t_out))
     w = q_weight if q_weight is not None else k_weight
     if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise ValueError("the weights must have one dtype")
@@ -565,11 +563,8 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
         R = 2 * inv_freq.shape[0]
         _ints("pos", pos, (B, T))
     dev = _here(q, k, q_out, k_out, pos, inv_freq, q_weight, k_weight)
-    v = _HeadViews(*views)
-    qr = (ctypes.byref(v), ctypes.byref(v, _VIEW)) if q is not None else (None, None)
-    kr = (ctypes.byref(v, 2 * _VIEW), ctypes.byref(v, 3 * _VIEW)) if k is not None else (None, None)
     rc = _lib.hqmq_qk_norm_rope(
-        *qr, *kr, _code(x), B, T, D, _addr(q_weight), _addr(k_weight), HQMQ_BF16 if w is None else _code(w),
+        *views, _code(x), B, T, D, _addr(q_weight), _addr(k_weight), HQMQ_BF16 if w is None else _code(w),
         eps, _addr(pos), _addr(inv_freq), R, 1 if interleaved else 0, _on(stream, dev))
     if rc:
         _check("hqmq_qk_norm_rope", rc)
