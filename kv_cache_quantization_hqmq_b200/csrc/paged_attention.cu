@@ -15,14 +15,14 @@
 //   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // k_paged_attn, warps by role:
-//   * three scout warps look the tiles' pages and flag words up and tell the
+//   * scout warps look the tiles' pages and flag words up and tell the
 //     producers where each token's codes and flagged values lie;
 //   * 16 producer warps decode codes from global memory (fetched two tiles
 //     ahead) through the head's codeword table in shared memory into bf16
 //     tiles [64 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
-//   * one warp's elected thread issues the products (tcgen05.mma, 128 rows, accumulators
+//   * a warp for every group of rows issues its products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
 //     softmax in base 2, P back as two bf16 terms P_hi + P_lo (about 16
@@ -43,13 +43,12 @@ constexpr int PA_D = 128;
 constexpr int PA_TILE = 64;                   // tokens of a tile
 constexpr int PA_PART = 132;                  // floats of a row's partial: m, l, -, -, O[128]
 constexpr int PA_CTAS = 148;                  // one per SM of a B200
-constexpr int OWN_COST = 2;                   // see prefix_cost
 constexpr int PA_REP_ROWS = 32;               // segments up to this many rows are replicated
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
 constexpr int META_RING = 4;                  // tiles
 constexpr int MASK_RING = 16;                 // the scouts are at most 10 tiles ahead of the softmax
-constexpr int PROD_WARPS = 16, SCOUTS = 3;
+constexpr int PROD_WARPS = 16;
 
 struct PagedAttnArgs {
     const uint16_t *q;
@@ -59,7 +58,6 @@ struct PagedAttnArgs {
     const int *seq_len, *table, *prefix_table;
     int max_pages, prefix_len;
     int row_tiles, prefix_tiles;              // segments of the prefix, tiles in each
-    int prefix_cost;                          // of a tile of the prefix; one of a sequence's own costs OWN_COST
     float sl2;                                // |scale| log2(e)
     uint32_t q_flip;                          // sign bits to flip in q (scale < 0)
     float *part_prefix, *part_own;            // [segment + CTA][rows][PA_PART]
@@ -94,49 +92,45 @@ __device__ __forceinline__ int64_t tiles_before(const PagedAttnArgs &a, int b_en
     return before;
 }
 
-// How the list of all heads' tiles is shared out: by cost, CTA c taking the
-// tiles that start in [c len, (c + 1) len).
+// How the list of all heads' tiles is shared out: CTA c takes the tiles
+// [c len, (c + 1) len).
 struct Shares {
-    int64_t per_head, total, len;
+    int64_t per_head, total;
+    uint32_t len;
     __device__ __forceinline__ Shares(const PagedAttnArgs &a, int64_t own_total) {
-        per_head = (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost + own_total * OWN_COST;
+        per_head = (int64_t)a.row_tiles * a.prefix_tiles + own_total;
         total = per_head * a.Hk;
-        len = total < (1ll << 31) ? (int64_t)(((uint32_t)total + PA_CTAS - 1) / PA_CTAS) : (total + PA_CTAS - 1) / PA_CTAS;
-        // (no less than a tile: the CTAs needed are no more than there are tiles)
-        len = max(len, (int64_t)max(a.prefix_tiles ? a.prefix_cost : 0, OWN_COST));
+        len = (uint32_t)max((total + PA_CTAS - 1) / PA_CTAS, (int64_t)1);
     }
-    __device__ __forceinline__ int owner(int64_t at) const {
-        return at < (1ll << 32) && len < (1ll << 32) ? (int)((uint32_t)at / (uint32_t)len) : (int)(at / len);
+    __device__ __forceinline__ int owner(int64_t tile) const {
+        return tile < (1ll << 32) ? (int)((uint32_t)tile / len) : (int)(tile / len);
     }
 };
 
 // A place in the list: tile `tile` of segment `seg` of `head`.
 struct Cursor {
-    int head, seg, tile, n_tiles;             // n_tiles of the segment
-    int64_t left;                             // cost from this tile's start to the end of the CTA's share
+    int head, seg, tile, n_tiles, left;       // tiles of the segment, tiles left of the CTA's share
     __device__ __forceinline__ bool prefix(const PagedAttnArgs &a) const { return seg < a.row_tiles; }
-    __device__ __forceinline__ int cost(const PagedAttnArgs &a) const { return prefix(a) ? a.prefix_cost : OWN_COST; }
-    __device__ __forceinline__ void settle(const PagedAttnArgs &a) {
-        while (left > 0 && tile >= n_tiles) {
-            tile = 0;
-            if (++seg == a.row_tiles + a.B) {
-                seg = 0;
-                if (++head == a.Hk) left = 0;
-            }
-            n_tiles = seg < a.row_tiles ? a.prefix_tiles : own_tiles(a, seg - a.row_tiles);
-        }
-    }
-    __device__ __forceinline__ int piece(const PagedAttnArgs &a) const {
-        const int c = cost(a);
-        const int64_t most = (left + c - 1) / c;
-        return most < n_tiles - tile ? (int)most : n_tiles - tile;
-    }
-    __device__ __forceinline__ void skip(const PagedAttnArgs &a, int n) {
-        left -= (int64_t)n * cost(a);
-        tile += n;
-        settle(a);
-    }
+    __device__ __forceinline__ int piece() const { return min(left, n_tiles - tile); }
+    __device__ __forceinline__ void skip(const PagedAttnArgs &a, int n);
 };
+// Over the segments that have no tiles left.
+__device__ __forceinline__ Cursor settled(const PagedAttnArgs &a, Cursor c) {
+    while (c.left > 0 && c.tile >= c.n_tiles) {
+        c.tile = 0;
+        if (++c.seg == a.row_tiles + a.B) {
+            c.seg = 0;
+            ++c.head;
+        }
+        c.n_tiles = c.seg < a.row_tiles ? a.prefix_tiles : own_tiles(a, c.seg - a.row_tiles);
+    }
+    return c;
+}
+__device__ __forceinline__ void Cursor::skip(const PagedAttnArgs &a, int n) {
+    tile += n;
+    left -= n;
+    if (tile >= n_tiles) *this = settled(a, *this);
+}
 
 // Rows of a segment, whether they are replicated, and its softmax groups.
 template <int MT> struct Rows {
@@ -181,20 +175,23 @@ template <int MT> struct Shared {
 };
 
 // Tensor memory columns.  One group of rows: O, Q, two S buffers, two P
-// buffers.  Two groups: O and Q of both, and per group 64 columns X that hold
-// S, and then P in its place; replicated rows, which use one group only, take
-// both X for S and the second group's O for their P buffers.
+// buffers.  Two groups: O and Q of both, and per group 64 columns for the
+// scores, each half of which its weights then replace; replicated rows, which
+// use one group only, take both for two S buffers and the second group's O for
+// their P buffers.  All 512 columns are allocated, so they start at address 0,
+// a constant in every product.
 template <int MT, int NT> struct Tmem {
     static constexpr uint32_t COLS = 512, P_COLS = 32 * NT;
-    __device__ __forceinline__ static uint32_t o(int g) { return g * 128; }
-    __device__ __forceinline__ static uint32_t q(int g) { return MT * 128 + g * 64; }
-    __device__ __forceinline__ static uint32_t s(int i) { return MT * 192 + i * 64; }
-    __device__ __forceinline__ static uint32_t p(int i) { return MT == 1 ? 320 + i * P_COLS : 128 + i * 64; }
-    static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64, "tensor memory");
+    __host__ __device__ static constexpr uint32_t o(int g) { return g * 128; }
+    __host__ __device__ static constexpr uint32_t q(int g) { return MT * 128 + g * 64; }
+    __host__ __device__ static constexpr uint32_t s(int i) { return MT * 192 + i * 64; }
+    __host__ __device__ static constexpr uint32_t half(int g, int h) { return MT * 192 + g * 64 + h * 32; }
+    __host__ __device__ static constexpr uint32_t p(int i) { return MT == 1 ? 320 + i * P_COLS : 128 + i * 64; }
+    static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64 && NT == 1, "tensor memory");
 };
-// Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P: halves of
-// 32 tokens, each over the columns of its own scores when P replaces S.
-template <int NT> __device__ __forceinline__ uint32_t p_col(int k, int t) { return (k >> 1) * 16 * NT + t * 16 + (k & 1) * 8; }
+// Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P, and where in P that replaces S.
+template <int NT> __host__ __device__ constexpr uint32_t p_col(int k, int t) { return (k >> 1) * 16 * NT + t * 16 + (k & 1) * 8; }
+__host__ __device__ constexpr uint32_t p_col_in_s(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -221,11 +218,11 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
 }
 
 // ---------------------------------------------------------------------------
-// scouts: warp s takes every third tile, lane l = its tokens 2 l and 2 l + 1
+// scouts: warp s of N takes every N-th tile, lane l = its tokens 2 l and 2 l + 1
 // ---------------------------------------------------------------------------
 // A tile's page ids are fetched two of the warp's tiles before it is handed
 // on, its flag words one.
-struct Scout {
+template <int SCOUTS> struct Scout {
     const PagedAttnArgs &a;
     const int lane;
     Cursor c;
@@ -251,9 +248,9 @@ struct Scout {
     }
     __device__ __forceinline__ void step(int n) {
         for (; n > 0 && c.left > 0; --n) {
-            c.left -= c.cost(a);
+            --c.left;
             if (++c.tile >= c.n_tiles) {
-                c.settle(a);
+                c = settled(a, c);
                 segment();
             }
         }
@@ -332,25 +329,24 @@ struct Scout {
 
 template <int MT>
 __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int which, int lane) {
-    Scout s(a, sh.start, lane, which);
+    constexpr int SCOUTS = 4 - MT;
+    Scout<SCOUTS> s(a, sh.start, lane, which);
     const int total = sh.total;
-    Scout::Tile x[2];
-    s.pages(x[0]);
-    s.pages(x[1]);
-    s.flags(x[0]);
-    for (int n = which; n < total; n += 2 * SCOUTS) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = n + i * SCOUTS;
-            if (t >= total) break;
-            const int slot = t % META_RING;
-            s.flags(x[1 - i]);
-            if (!mbar_wait(&sh.meta_empty[slot], ((t / META_RING) & 1) ^ 1)) return false;
-            s.hand_on(x[i], sh.meta[slot], &sh.mask[t % MASK_RING]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.meta_full[slot]);
-            s.pages(x[i]);
-        }
+    typename Scout<SCOUTS>::Tile now, next;   // (flag words under way; page ids under way)
+    next.head = -1;
+    // the first two rounds only fill the pipeline
+#pragma unroll 1
+    for (int t = which - 2 * SCOUTS; t < total; t += SCOUTS) {
+        const typename Scout<SCOUTS>::Tile x = now;
+        now = next;
+        s.flags(now);
+        s.pages(next);
+        if (t < which) continue;
+        const int slot = t % META_RING;
+        if (!mbar_wait(&sh.meta_empty[slot], ((t / META_RING) & 1) ^ 1)) return false;
+        s.hand_on(x, sh.meta[slot], &sh.mask[t % MASK_RING]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_full[slot]);
     }
     return true;
 }
@@ -516,27 +512,26 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
     Slot<BT> x, next;
 
     next.head = head;
+    // the first round only fetches; one round past the end meets the heads that are left
 #pragma unroll 1
-    for (int n = st - 2; n < total; n += 2) {
+    for (int n = st - 2; n < total + 2; n += 2) {
         x = next;
+        next.head = last_head;
         if (n + 2 < total) {
             const int r = (n + 2) % META_RING;
             if (!mbar_wait(&sh.meta_full[r], ((n + 2) / META_RING) & 1)) return false;
             pr.fetch(next, sh.meta[r]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_empty[r]);
-        } else {
-            next.head = last_head;
         }
         // every producer passes through every head: they meet, build its tables and meet again
-        const int to = n < 0 ? head : x.head;
-        while (head < to) {
+        while (n >= 0 && head < x.head) {
             if (!meet(sh.heads, meetings, lane)) return false;
             ++head;
             build_table(p, R, head, table, (st * 4 + sub) * 32 + lane);
             if (!meet(sh.heads, meetings, lane)) return false;
         }
-        if (n < 0) continue;
+        if (n < 0 || n >= total) continue;
         if (!mbar_wait(empty, par)) return false;
         par ^= 1u;
         pr.decode(x, tile);
@@ -544,116 +539,137 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
     }
-    while (head < last_head) {
-        if (!meet(sh.heads, meetings, lane)) return false;
-        ++head;
-        build_table(p, R, head, table, (st * 4 + sub) * 32 + lane);
-        if (!meet(sh.heads, meetings, lane)) return false;
-    }
     return true;
 }
 
 // ---------------------------------------------------------------------------
 // the matrix products: one thread
 // ---------------------------------------------------------------------------
+// Everything in a product but its barrier is known at compile time (stage,
+// buffer, group, the start of shared memory): operands that have to be brought
+// to uniform registers for every product made the issue, not the tensor core,
+// the limit (two groups: 90 and 50 clocks a product in a loop and unrolled).
 template <int MT, int NT> struct Products {
     using TM = Tmem<MT, NT>;
-    Shared<MT> &sh;
-    const uint32_t tmem, tiles;
     const bool leader;
 
-    // S = Q K^T of the K tile in stage st; arrives on s_full.
-    __device__ __forceinline__ void scores(int g, uint32_t s, int st, uint64_t *done) {
+    // S = Q K^T of the K tile in stage ST; arrives on `done`.
+    template <int G, int ST, uint32_t S> __device__ __forceinline__ void scores(uint64_t *done) const {
+        extern __shared__ __align__(1024) uint8_t dyn[];
         constexpr uint32_t idesc = mma_idesc(128, PA_TILE, false);
         tc_fence_after();
         if (leader) {
+            const uint64_t d = smem_desc(smem_addr(dyn) + ST * TILE_BYTES, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mma_ts(tmem + s, tmem + TM::q(g) + k * 8,
-                       smem_desc(tiles + st * TILE_BYTES + (k >> 2) * (TILE_BYTES / 2) + (k & 3) * 32, 16, 1024), idesc,
-                       k > 0);
+            for (int k = 0; k < 8; ++k)       // 16 elements: 32 bytes of a row, the second 64 in the next block
+                mma_ts(S, TM::q(G) + k * 8, d + (k >> 2) * (TILE_BYTES / 2 / 16) + (k & 3) * 2, idesc, k > 0);
             mma_commit(done);
         }
     }
-    // O (+)= P V of the V tile in stage st; arrives on p_empty.
-    __device__ __forceinline__ void output(int g, uint32_t p, int st, bool add, uint64_t *done) {
+    // O (+)= P V of the V tile in stage ST; arrives on `done`.
+    template <int G, int ST, uint32_t P, bool IN_S> __device__ __forceinline__ void output(bool add, uint64_t *done) const {
+        extern __shared__ __align__(1024) uint8_t dyn[];
         constexpr uint32_t idesc = mma_idesc(128, PA_D, true);
         tc_fence_after();
         if (leader) {
+            const uint64_t d = smem_desc(smem_addr(dyn) + (2 + ST) * TILE_BYTES, TILE_BYTES / 2, 1024);
 #pragma unroll
-            for (int k = 0; k < PA_TILE / 16; ++k) {
-                const uint64_t d = smem_desc(tiles + (2 + st) * TILE_BYTES + k * 2048, TILE_BYTES / 2, 1024);
+            for (int k = 0; k < PA_TILE / 16; ++k)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    mma_ts(tmem + TM::o(g), tmem + p + p_col<NT>(k, t), d, idesc, add || k > 0 || t > 0);
-            }
+                    mma_ts(TM::o(G), P + (IN_S ? p_col_in_s(k) : p_col<NT>(k, t)), d + k * 128, idesc,
+                           k || t ? 1u : (uint32_t)add);
             mma_commit(done);
         }
     }
 };
 
-template <int MT, int NT>
-__device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles,
-                                               bool leader) {
-    using TM = Tmem<MT, NT>;
-    Products<MT, NT> pr = {sh, __shfl_sync(FULL, sh.tmem, 0), tiles, leader};
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(FULL, mbar_wait(bar, parity));
+}
+
+// The next tile's scores, if there is one, and P V of this tile, for a group
+// with one buffer: P replaces S, so the scores wait for P V.
+template <int MT, int NT, int G, int ST>
+__device__ __forceinline__ bool pair_scores(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t ph) {
+    if (!all_wait(&sh.k_full[ST], (tile >> 1) & 1)) return false;
+    if (!all_wait(&sh.p_empty[G][0], (ph & 1) ^ 1)) return false;
+    pr.template scores<G, ST, Tmem<MT, NT>::half(G, 0)>(&sh.s_full[G][0]);
+    if (pr.leader) mma_commit(&sh.k_empty[ST]);
+    return true;
+}
+template <int MT, int NT, int G, int ST>
+__device__ __forceinline__ bool pair_output(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t &ph, bool add) {
+    if (!all_wait(&sh.v_full[ST], (tile >> 1) & 1)) return false;
+    if (!all_wait(&sh.p_full[G][0], ph & 1)) return false;
+    pr.template output<G, ST, Tmem<MT, NT>::half(G, 0), true>(add, &sh.p_empty[G][0]);
+    if (pr.leader) mma_commit(&sh.v_empty[ST]);
+    ph ^= 1u;
+    return true;
+}
+// The same for one group with two buffers of S and P (buffer = stage).
+template <int MT, int NT, int ST>
+__device__ __forceinline__ bool tile_scores(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t ph) {
+    if (!all_wait(&sh.k_full[ST], (tile >> 1) & 1)) return false;
+    if (!all_wait(&sh.s_empty[0][ST], ((ph >> ST) & 1) ^ 1)) return false;
+    pr.template scores<0, ST, Tmem<MT, NT>::s(ST)>(&sh.s_full[0][ST]);
+    if (pr.leader) mma_commit(&sh.k_empty[ST]);
+    return true;
+}
+template <int MT, int NT, int ST>
+__device__ __forceinline__ bool tile_output(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t &ph, bool add) {
+    if (!all_wait(&sh.v_full[ST], (tile >> 1) & 1)) return false;
+    if (!all_wait(&sh.p_full[0][ST], (ph >> ST) & 1)) return false;
+    pr.template output<0, ST, Tmem<MT, NT>::p(ST), false>(add, &sh.p_empty[0][ST]);
+    if (pr.leader) mma_commit(&sh.v_empty[ST]);
+    ph ^= 1u << ST;
+    return true;
+}
+
+// One warp for each group G of rows.  Every warp takes part in every tile: a
+// stage is free when all of them have let go of it.
+template <int MT, int NT, int G>
+__device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, bool leader) {
+    const Products<MT, NT> pr = {leader};
     Cursor c = sh.start;
     int no = 0;                               // tiles so far: stage no % 2, phase no / 2
-    uint32_t ph[MT], pq = 0;                  // phases of the groups' two buffers, and of q_full
-#pragma unroll
-    for (int g = 0; g < MT; ++g) ph[g] = 0;
-    while (c.left > 0) {
-        const int n = c.piece(a);
+    uint32_t ph = 0, pq = 0;                  // phases of the group's two buffers, and of q_full
+    while (__shfl_sync(FULL, c.left > 0, 0)) {
+        const int n = __shfl_sync(FULL, c.piece(), 0);
         const Rows<MT> rows(a, c);
-        const int groups = rows.groups();
-#pragma unroll
-        for (int g = 0; g < MT; ++g) {
-            if (g >= groups) continue;
-            if (!mbar_wait(&sh.q_full[g], (pq >> g) & 1)) return false;
-            pq ^= 1u << g;
+        const bool mine = __shfl_sync(FULL, G < rows.groups(), 0), rep = __shfl_sync(FULL, rows.rep, 0);
+        if (mine) {
+            if (!all_wait(&sh.q_full[G], pq)) return false;
+            pq ^= 1u;
         }
-        if (MT == 1 || rows.rep) {
-            // S of tile i before P V of tile i - 1: the softmax has two buffers of each
-            uint32_t f = ph[0];
-            for (int i = 0; i <= n; ++i) {
-                if (i < n) {
-                    const int b = i & 1, st = (no + i) & 1;
-                    if (!mbar_wait(&sh.k_full[st], ((no + i) >> 1) & 1)) return false;
-                    if (!mbar_wait(&sh.s_empty[0][b], ((f >> b) & 1) ^ 1)) return false;
-                    pr.scores(0, TM::s(b), st, &sh.s_full[0][b]);
-                    if (leader) mma_commit(&sh.k_empty[st]);
-                }
-                if (i > 0) {
-                    const int j = i - 1, b = j & 1, st = (no + j) & 1;
-                    if (!mbar_wait(&sh.v_full[st], ((no + j) >> 1) & 1)) return false;
-                    if (!mbar_wait(&sh.p_full[0][b], (ph[0] >> b) & 1)) return false;
-                    pr.output(0, TM::p(b), st, j > 0, &sh.p_empty[0][b]);
-                    if (leader) mma_commit(&sh.v_empty[st]);
-                    ph[0] ^= 1u << b;
-                }
-                if (i < n) f ^= 1u << (i & 1);
+        if (!mine) {
+            for (int t = no; t < no + n; ++t) {
+                if (!all_wait(&sh.k_full[t & 1], (t >> 1) & 1)) return false;
+                if (leader) mbar_arrive(&sh.k_empty[t & 1]);
+                if (!all_wait(&sh.v_full[t & 1], (t >> 1) & 1)) return false;
+                if (leader) mbar_arrive(&sh.v_empty[t & 1]);
             }
-        } else {
-            // P takes the place of S: a group's next scores wait for its P V
+        } else if (G == 0 && (MT == 1 || rep)) {
+            // scores of tile i before P V of tile i - 1
+            uint32_t f = ph;                  // phases as the scores see them, a tile ahead
             for (int i = 0; i <= n; ++i) {
-                const int st = (no + i) & 1, sv = (no + i - 1) & 1;
-                if (i < n && !mbar_wait(&sh.k_full[st], ((no + i) >> 1) & 1)) return false;
-                if (i > 0 && !mbar_wait(&sh.v_full[sv], ((no + i - 1) >> 1) & 1)) return false;
-#pragma unroll
-                for (int g = 0; g < MT; ++g) {
-                    if (g >= groups) continue;
-                    if (i > 0) {
-                        if (!mbar_wait(&sh.p_full[g][0], ph[g] & 1)) return false;
-                        pr.output(g, TM::s(g), sv, i > 1, &sh.p_empty[g][0]);
-                        ph[g] ^= 1u;
-                    }
-                    if (i < n) {
-                        if (!mbar_wait(&sh.p_empty[g][0], (ph[g] & 1) ^ 1)) return false;
-                        pr.scores(g, TM::s(g), st, &sh.s_full[g][0]);
-                    }
+                const int t = no + i;
+                if (i < n) {
+                    if (!(t & 1 ? tile_scores<MT, NT, 1>(pr, sh, t, f) : tile_scores<MT, NT, 0>(pr, sh, t, f))) return false;
+                    f ^= 1u << (t & 1);
                 }
-                if (leader && i > 0) mma_commit(&sh.v_empty[sv]);
-                if (leader && i < n) mma_commit(&sh.k_empty[st]);
+                if (i > 0 && !(t & 1 ? tile_output<MT, NT, 0>(pr, sh, t - 1, ph, i > 1)
+                                     : tile_output<MT, NT, 1>(pr, sh, t - 1, ph, i > 1)))
+                    return false;
+            }
+        } else if (MT == 2) {
+            for (int i = 0; i <= n; ++i) {
+                const int t = no + i;
+                if (i > 0 && !(t & 1 ? pair_output<MT, NT, G, 0>(pr, sh, t - 1, ph, i > 1)
+                                     : pair_output<MT, NT, G, 1>(pr, sh, t - 1, ph, i > 1)))
+                    return false;
+                if (i < n && !(t & 1 ? pair_scores<MT, NT, G, 1>(pr, sh, t, ph) : pair_scores<MT, NT, G, 0>(pr, sh, t, ph)))
+                    return false;
             }
         }
         no += n;
@@ -781,9 +797,8 @@ template <int MT, int NT> struct Softmax {
         for (int t = 0; t < NT; ++t) tmem_st8(p + 16 * t, w[t]);
     }
 
-    // Replicated rows: 16 of the tile's columns.
-    __device__ __forceinline__ bool tile_rep(int i, const uint2 &valid) {
-        const int b = i & 1;
+    // Replicated rows: 16 of the columns of the piece's tile i, in buffer b.
+    __device__ __forceinline__ bool tile_rep(int i, int b, const uint2 &valid) {
         if (!mbar_wait(&sh.s_full[0][b], (ph >> b) & 1)) return false;
         tc_fence_after();
         const uint32_t mask = ((quad & 2 ? valid.y : valid.x) >> (16 * (quad & 1))) & 0xFFFFu;
@@ -801,15 +816,42 @@ template <int MT, int NT> struct Softmax {
         ph ^= 1u << b;
         return true;
     }
-    // A row per thread: all 64 columns, in halves, read once for the maximum and again for the weights.
-    __device__ __forceinline__ bool tile_full(int i, const uint2 &valid) {
-        const int b = MT == 1 ? i & 1 : 0;
+    // A row per thread, one group: all 64 columns of tile i, in buffer b.
+    __device__ __forceinline__ bool tile_full(int i, int b, const uint2 &valid) {
         if (!mbar_wait(&sh.s_full[g][b], (ph >> b) & 1)) return false;
         tc_fence_after();
         const uint2 mask = valid;
-        const uint32_t ts = lanes + TM::s(MT == 1 ? b : g), tp = MT == 1 ? lanes + TM::p(b) : ts;
-        float mt = -INFINITY;
+        uint32_t s0[32], s1[32];
+        tmem_ld32(lanes + TM::s(b), s0);
+        tmem_ld32(lanes + TM::s(b) + 32, s1);
+        tmem_wait_ld();
+        arrive(&sh.s_empty[g][b]);
+        if (mask.x != FULL) hide(s0, mask.x);
+        if (mask.y != FULL) hide(s1, mask.y);
+        if (!rescale(fmaxf(row_max<32>(s0), row_max<32>(s1)), i > 0 ? &sh.p_empty[g][b ^ 1] : nullptr,
+                     ((ph >> (b ^ 1)) & 1) ^ 1))
+            return false;
+        if (!mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
+        tc_fence_after();
+        const float rf = ref == -INFINITY ? 0.f : ref;
+        const uint32_t tp = lanes + TM::p(b);
+        put(s0, rf, tp + p_col<NT>(0, 0));
+        put(s0 + 16, rf, tp + p_col<NT>(1, 0));
+        put(s1, rf, tp + p_col<NT>(2, 0));
+        put(s1 + 16, rf, tp + p_col<NT>(3, 0));
+        tmem_wait_st();
+        arrive(&sh.p_full[g][b]);
+        ph ^= 1u << b;
+        return true;
+    }
+    // A row per thread, two groups: the piece's tile i, its weights in the place of its scores.
+    __device__ __forceinline__ bool tile_pair(int i, const uint2 &valid) {
+        if (!mbar_wait(&sh.s_full[g][0], ph & 1)) return false;
+        tc_fence_after();
+        const uint2 mask = valid;
+        const uint32_t ts = lanes + TM::half(g, 0);
         uint32_t s[32];
+        float mt = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             tmem_ld32(ts + 32 * h, s);
@@ -818,28 +860,23 @@ template <int MT, int NT> struct Softmax {
             if (w != FULL) hide(s, w);
             mt = fmaxf(mt, row_max<32>(s));
         }
-        // with one buffer the scores were issued after the products before them had ended
-        uint64_t *done = i == 0 ? nullptr : &sh.p_empty[g][MT == 1 ? b ^ 1 : 0];
-        if (!rescale(mt, done, (MT == 1 ? (ph >> (b ^ 1)) & 1 : ph & 1) ^ 1)) return false;
-        if (MT == 1) {
-            if (!mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
-            tc_fence_after();
-        }
+        // (the scores were issued after the products before them had ended)
+        if (!rescale(mt, i > 0 ? &sh.p_empty[g][0] : nullptr, (ph & 1) ^ 1)) return false;
         const float rf = ref == -INFINITY ? 0.f : ref;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            tmem_ld32(ts + 32 * h, s);
-            tmem_wait_ld();
-            if (MT == 1 && h == 1) arrive(&sh.s_empty[g][b]);
-            const uint32_t w = h ? mask.y : mask.x;
-            if (w != FULL) hide(s, w);
-            put(s, rf, tp + p_col<NT>(2 * h, 0));
-            put(s + 16, rf, tp + p_col<NT>(2 * h + 1, 0));
+        for (int h = 1; h >= 0; --h) {        // (the second half's scores are still there)
+            put(s, rf, ts + 32 * h);
+            put(s + 16, rf, ts + 32 * h + 8);
+            if (h) {
+                tmem_ld32(ts, s);
+                tmem_wait_ld();
+                if (mask.x != FULL) hide(s, mask.x);
+            }
         }
         tmem_wait_st();
-        if (MT == 2) arrive(&sh.s_empty[g][b]);
-        arrive(&sh.p_full[g][b]);
-        ph ^= 1u << b;
+        arrive(&sh.s_empty[g][0]);            // (for the replicated pieces, which wait for it)
+        arrive(&sh.p_full[g][0]);
+        ph ^= 1u;
         return true;
     }
 };
@@ -848,30 +885,30 @@ template <int MT, int NT>
 __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, int warp, int lane) {
     using TM = Tmem<MT, NT>;
     const int quad = warp & 3;
-    Softmax<MT, NT> sm = {a, sh, warp >> 2, quad, lane, sh.tmem + ((uint32_t)(quad * 32) << 16), 0.f, 0.f,
+    Softmax<MT, NT> sm = {a, sh, warp >> 2, quad, lane, (uint32_t)(quad * 32) << 16, 0.f, 0.f,
                           make_float2(0.f, 0.f), 0u};
     const int g = sm.g;
     Cursor c = sh.start;
     int no = 0, pairs = 0;                    // tiles, and pieces of two groups, so far
     bool cleared = false;                     // P is zero outside this quarter's columns
     while (c.left > 0) {
-        const int n = c.piece(a);
+        const int n = c.piece();
         const Rows<MT> rows(a, c);
-        if (g >= rows.groups()) {
-            no += n;
-            c.skip(a, n);
-            continue;
-        }
+        const Cursor at = c;
+        const int t0 = no;                    // the piece's first tile
+        no += n;
+        c.skip(a, n);
+        if (g >= rows.groups()) continue;
         const int r = rows.rep ? lane : g * 128 + quad * 32 + lane;
         const bool live = r < rows.n;
-        const bool pre = c.prefix(a);
+        const bool pre = at.prefix(a);
         // the rows' queries
         {
             // (replicated rows keep P where the second group had O)
             if (MT == 2 && rows.rep && pairs > 0 && !mbar_wait(&sh.pair_done, (pairs - 1) & 1)) return false;
             const int gr = rows.base + r;
-            const size_t qr = pre ? ((size_t)(gr / a.G) * a.Hk + c.head) * a.G + gr % a.G
-                                  : ((size_t)(c.seg - a.row_tiles) * a.Hk + c.head) * a.G + r;
+            const size_t qr = pre ? ((size_t)(gr / a.G) * a.Hk + at.head) * a.G + gr % a.G
+                                  : ((size_t)(at.seg - a.row_tiles) * a.Hk + at.head) * a.G + r;
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qr * PA_D);
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
@@ -901,16 +938,19 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
         sm.l = make_float2(0.f, 0.f);
         if (rows.rep) {
             for (int i = 0; i < n; ++i)
-                if (!sm.tile_rep(i, sh.mask[(no + i) % MASK_RING])) return false;
+                if (!sm.tile_rep(i, (t0 + i) & 1, sh.mask[(t0 + i) % MASK_RING])) return false;
+        } else if (MT == 1) {
+            for (int i = 0; i < n; ++i)
+                if (!sm.tile_full(i, (t0 + i) & 1, sh.mask[(t0 + i) % MASK_RING])) return false;
         } else {
             for (int i = 0; i < n; ++i)
-                if (!sm.tile_full(i, sh.mask[(no + i) % MASK_RING])) return false;
+                if (!sm.tile_pair(i, sh.mask[(t0 + i) % MASK_RING])) return false;
         }
         // the piece's partial
-        const int lb = MT == 1 || rows.rep ? (n - 1) & 1 : 0;
+        const int lb = MT == 1 || rows.rep ? (no - 1) & 1 : 0;
         if (!mbar_wait(&sh.p_empty[g][lb], ((sm.ph >> lb) & 1) ^ 1)) return false;
         tc_fence_after();
-        const int seg = pre ? c.head * a.row_tiles + c.seg : c.head * a.B + c.seg - a.row_tiles;
+        const int seg = pre ? at.head * a.row_tiles + at.seg : at.head * a.B + at.seg - a.row_tiles;
         const int slot_rows = pre ? a.prefix_slot_rows : a.own_slot_rows;
         const int srow = rows.rep ? quad * rows.n + lane : r;
         float *dst = (pre ? a.part_prefix : a.part_own) +
@@ -932,18 +972,16 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             ++pairs;
             if (g == 1) sm.arrive(&sh.pair_done);
         }
-        no += n;
-        c.skip(a, n);
     }
     return true;
 }
 
-// Warps: 4 MT softmax, 16 producers, three scouts, the products.  The block is
-// launched with REGS a thread, and each group of four warps takes what it
+// Warps: 4 MT softmax, 16 producers, 4 - MT scouts, MT for the products.  The
+// block is launched with REGS a thread, and each group of four warps takes what it
 // needs of their sum.
 template <int MT> struct Roles {
-    static constexpr int SCOUT = 4 * MT + PROD_WARPS, PRODUCTS = SCOUT + SCOUTS;
-    static constexpr int THREADS = (PRODUCTS + 1) * 32;
+    static constexpr int SCOUT = 4 * MT + PROD_WARPS, PRODUCTS = SCOUT + 4 - MT;
+    static constexpr int THREADS = (PRODUCTS + MT) * 32;
     static constexpr int REGS = MT == 1 ? 80 : 72;
     static constexpr int SOFTMAX = MT == 1 ? 128 : 80, PRODUCER = 72, REST = MT == 1 ? 64 : 56;
     static_assert(REGS * THREADS <= 65536, "registers of an SM");
@@ -966,8 +1004,8 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh.k_full[i], PROD_WARPS / 4);
                 mbar_init(&sh.v_full[i], PROD_WARPS / 4);
-                mbar_init(&sh.k_empty[i], 1);
-                mbar_init(&sh.v_empty[i], 1);
+                mbar_init(&sh.k_empty[i], MT);
+                mbar_init(&sh.v_empty[i], MT);
             }
             for (int g = 0; g < MT; ++g) {
                 mbar_init(&sh.q_full[g], 4);
@@ -984,7 +1022,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             }
             mbar_init(&sh.pair_done, 4);
             mbar_init(&sh.heads, PROD_WARPS);
-            mbar_init(&sh.drain, 1);
+            mbar_init(&sh.drain, MT);
             mbar_init_fence();
         }
     }
@@ -994,23 +1032,21 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         tiles_before(a, 0, &own_total);
         const Shares w(a, own_total);
         Cursor c = {0, 0, 0, 0, 0};
-        const int64_t from = blockIdx.x * w.len;
+        const int64_t from = (int64_t)blockIdx.x * w.len;
         if (from < w.total) {
-            c.left = min(w.len, w.total - from);
+            c.left = (int)min((int64_t)w.len, w.total - from);
             c.head = (int)(from / w.per_head);
             int64_t rem = from - c.head * w.per_head;
-            const int64_t pre = (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost;
-            int64_t at = 0;                   // cost from the segment's start
+            const int64_t pre = (int64_t)a.row_tiles * a.prefix_tiles;
             if (rem < pre) {
-                const int64_t seg = (int64_t)a.prefix_tiles * a.prefix_cost;
-                c.seg = (int)(rem / seg);
+                c.seg = (int)(rem / a.prefix_tiles);
                 c.n_tiles = a.prefix_tiles;
-                at = rem - c.seg * seg;
+                c.tile = (int)(rem - (int64_t)c.seg * a.prefix_tiles);
             } else {
                 rem -= pre;
                 for (int b0 = 0; b0 < a.B; b0 += 32) {
                     const int n = b0 + lane < a.B ? own_tiles(a, b0 + lane) : 0;
-                    int64_t inc = (int64_t)n * OWN_COST;
+                    int64_t inc = n;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int64_t u = __shfl_up_sync(FULL, inc, o);
@@ -1021,28 +1057,16 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
                         const int src = __ffs(hit) - 1;
                         c.seg = a.row_tiles + b0 + src;
                         c.n_tiles = __shfl_sync(FULL, n, src);
-                        at = rem - __shfl_sync(FULL, inc - (int64_t)n * OWN_COST, src);
+                        c.tile = (int)(rem - __shfl_sync(FULL, inc - n, src));
                         break;
                     }
                     rem -= __shfl_sync(FULL, inc, 31);
                 }
             }
-            // the first tile that starts in the share
-            const int cost = c.cost(a);
-            c.tile = (int)((at + cost - 1) / cost);
-            c.left -= (int64_t)c.tile * cost - at;
-            c.settle(a);
-        }
-        int total = 0, last = c.head - 1;
-        for (Cursor d = c; d.left > 0;) {
-            const int n = d.piece(a);
-            total += n;
-            last = d.head;
-            d.skip(a, n);
         }
         if (lane == 0) {
-            sh.total = total;
-            sh.last_head = last;
+            sh.total = c.left;
+            sh.last_head = c.left > 0 ? (int)((from + c.left - 1) / w.per_head) : 0;
         }
         if (lane == 0) sh.start = c;
     }
@@ -1063,7 +1087,8 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             ok = scout<MT>(a, sh, warp - SCOUT, lane);
         } else {
             const bool leader = elect_one();
-            ok = issue_products<MT, NT>(a, sh, tiles, leader);
+            ok = sh.tmem == 0u && (warp == PRODUCTS ? issue_products<MT, NT, 0>(a, sh, leader)
+                                                    : issue_products<MT, NT, MT - 1>(a, sh, leader));
             if (leader) mma_commit(&sh.drain);    // nothing may be in flight when tensor memory goes
             if (!mbar_wait(&sh.drain, 0)) ok = false;
         }
@@ -1098,8 +1123,8 @@ k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
     if (a.prefix_tiles) {
         const int r = b * a.G + g, rt = r / (128 * MT);
         const bool rep = a.rows <= PA_REP_ROWS;
-        const int64_t at = head0 + (int64_t)rt * a.prefix_tiles * a.prefix_cost;
-        const int c0 = w.owner(at), c1 = w.owner(at + (int64_t)(a.prefix_tiles - 1) * a.prefix_cost);
+        const int64_t at = head0 + (int64_t)rt * a.prefix_tiles;
+        const int c0 = w.owner(at), c1 = w.owner(at + (a.prefix_tiles - 1));
         copies = rep ? 4 : 1;
         stride = a.rows * PA_PART;
         n_pre = (c1 - c0 + 1) * copies;
@@ -1107,8 +1132,8 @@ k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
         pre = a.part_prefix + ((size_t)head * a.row_tiles + rt + c0) * pre_step + (rep ? r : r % (128 * MT)) * PA_PART;
     }
     if (const int n = own_tiles(a, b)) {
-        const int64_t at = head0 + (int64_t)a.row_tiles * a.prefix_tiles * a.prefix_cost + before * OWN_COST;
-        const int c0 = w.owner(at), c1 = w.owner(at + (int64_t)(n - 1) * OWN_COST);
+        const int64_t at = head0 + (int64_t)a.row_tiles * a.prefix_tiles + before;
+        const int c0 = w.owner(at), c1 = w.owner(at + (n - 1));
         n_own = (c1 - c0 + 1) * 4;
         own_step = (size_t)a.own_slot_rows * PA_PART;
         own = a.part_own + ((size_t)head * a.B + b + c0) * own_step + g * PA_PART;
@@ -1243,7 +1268,6 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
     a.prefix_tiles = (prefix_len + PA_TILE - 1) / PA_TILE;
     const double sl2 = (double)scale * 1.4426950408889634;
     a.sl2 = fmaxf((float)(sl2 < 0 ? -sl2 : sl2), 1.2e-38f);  // (above 0, so that -inf stays -inf)
-    a.prefix_cost = a.rows <= PA_REP_ROWS ? OWN_COST : OWN_COST;
     a.q_flip = scale < 0 ? 0x80008000u : 0u;
     a.part_prefix = reinterpret_cast<float *>(ws);
     a.part_own = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + p.prefix_bytes);

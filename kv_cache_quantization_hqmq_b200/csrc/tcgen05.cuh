@@ -20,24 +20,24 @@ __device__ __forceinline__ void mbar_init_fence() {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("{.reg .b64 s;\n\tmbarrier.arrive.shared::cta.b64 s, [%0];}" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
+// Waits until the phase of the given parity has completed; false after 2^22
+// looks (a tenth of a second or more: each look waits a while by itself), upon
+// which the caller gives up.  A few instructions: a kernel of many roles has
+// many waits, and its code has to stay in the instruction cache.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{.reg .pred p;\n\t"
+    asm volatile("{.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+                 "mov.u32 n, 0;\n"
+                 "LOOK:\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "@p bra DONE;\n\t"
+                 "add.u32 n, n, 1;\n\t"
+                 "setp.lt.u32 q, n, 4194304;\n\t"
+                 "@q bra LOOK;\n"
+                 "DONE:\n\t"
                  "selp.u32 %0, 1, 0, p;}"
                  : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
     return ok != 0;
-}
-
-// Waits until the phase of the given parity has completed; false after about
-// two seconds (2^32 clocks), upon which the caller gives up.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    do {
-        if (mbar_try(bar, parity)) return true;
-    } while (clock64() - t0 < (1ll << 32));
-    return false;
 }
 
 // Shared-memory writes of this thread become visible to the tensor core.
