@@ -22,7 +22,7 @@
 //     tiles [64 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
-//   * a warp for every group of rows issues its products (tcgen05.mma, 128 rows, accumulators
+//   * two threads issue the products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
 //     softmax in base 2, P back as two bf16 terms P_hi + P_lo (about 16
@@ -150,6 +150,18 @@ template <int MT> struct Rows {
     __device__ __forceinline__ int groups() const { return rep ? 1 : (n + 127) / 128; }
 };
 
+// Warps: 4 MT softmax, 16 producers, two scouts, two for the products.  The
+// block is launched with REGS a thread, and each group of four warps takes what it
+// needs of their sum.
+template <int MT> struct Roles {
+    static constexpr int SCOUT = 4 * MT + PROD_WARPS, SCOUTS = 2, PRODUCTS = SCOUT + SCOUTS;
+    static constexpr int THREADS = (PRODUCTS + 2) * 32;
+    static constexpr int REGS = MT == 1 ? 80 : 72;
+    static constexpr int SOFTMAX = MT == 1 ? 128 : 80, PRODUCER = 72, REST = MT == 1 ? 64 : 56;
+    static_assert(REGS * THREADS <= 65536, "registers of an SM");
+    static_assert(128 * MT * SOFTMAX + 32 * PROD_WARPS * PRODUCER + 128 * REST <= REGS * THREADS, "register shares");
+};
+
 // What a scout warp finds out about a tile.
 struct Meta {
     long long page[PA_TILE / 16];             // page * heads + head of every 16 tokens
@@ -165,7 +177,7 @@ template <int MT> struct Shared {
     uint64_t meta_full[META_RING], meta_empty[META_RING];
     uint64_t pair_done;                                 // the second group has left a piece of two groups
     uint64_t heads;                                     // the producers, at a change of heads
-    uint64_t drain;
+    uint64_t drain[2];
     Meta meta[META_RING];
     uint2 mask[MASK_RING];                              // valid tokens of the last tiles
     Cursor start;
@@ -175,10 +187,10 @@ template <int MT> struct Shared {
 };
 
 // Tensor memory columns.  One group of rows: O, Q, two S buffers, two P
-// buffers.  Two groups: O and Q of both, and per group 64 columns for the
-// scores, each half of which its weights then replace; replicated rows, which
-// use one group only, take both for two S buffers and the second group's O for
-// their P buffers.  All 512 columns are allocated, so they start at address 0,
+// buffers.  Two groups: O and Q of both, and per group two buffers of 32
+// columns for the scores of half a tile, which their weights then replace;
+// replicated rows, which use one group only, take all four for two S buffers
+// and the second group's O for their P buffers.  All 512 columns are allocated, so they start at address 0,
 // a constant in every product.
 template <int MT, int NT> struct Tmem {
     static constexpr uint32_t COLS = 512, P_COLS = 32 * NT;
@@ -189,9 +201,8 @@ template <int MT, int NT> struct Tmem {
     __host__ __device__ static constexpr uint32_t p(int i) { return MT == 1 ? 320 + i * P_COLS : 128 + i * 64; }
     static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64 && NT == 1, "tensor memory");
 };
-// Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P, and where in P that replaces S.
+// Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P.
 template <int NT> __host__ __device__ constexpr uint32_t p_col(int k, int t) { return (k >> 1) * 16 * NT + t * 16 + (k & 1) * 8; }
-__host__ __device__ constexpr uint32_t p_col_in_s(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -329,7 +340,7 @@ template <int SCOUTS> struct Scout {
 
 template <int MT>
 __device__ __forceinline__ bool scout(const PagedAttnArgs &a, Shared<MT> &sh, int which, int lane) {
-    constexpr int SCOUTS = 4 - MT;
+    constexpr int SCOUTS = Roles<MT>::SCOUTS;
     Scout<SCOUTS> s(a, sh.start, lane, which);
     const int total = sh.total;
     typename Scout<SCOUTS>::Tile now, next;   // (flag words under way; page ids under way)
@@ -545,134 +556,98 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
 // ---------------------------------------------------------------------------
 // the matrix products: one thread
 // ---------------------------------------------------------------------------
-// Everything in a product but its barrier is known at compile time (stage,
-// buffer, group, the start of shared memory): operands that have to be brought
-// to uniform registers for every product made the issue, not the tensor core,
-// the limit (two groups: 90 and 50 clocks a product in a loop and unrolled).
-template <int MT, int NT> struct Products {
-    using TM = Tmem<MT, NT>;
-    const bool leader;
-
-    // S = Q K^T of the K tile in stage ST; arrives on `done`.
-    template <int G, int ST, uint32_t S> __device__ __forceinline__ void scores(uint64_t *done) const {
-        extern __shared__ __align__(1024) uint8_t dyn[];
-        constexpr uint32_t idesc = mma_idesc(128, PA_TILE, false);
-        tc_fence_after();
-        if (leader) {
-            const uint64_t d = smem_desc(smem_addr(dyn) + ST * TILE_BYTES, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)       // 16 elements: 32 bytes of a row, the second 64 in the next block
-                mma_ts(S, TM::q(G) + k * 8, d + (k >> 2) * (TILE_BYTES / 2 / 16) + (k & 3) * 2, idesc, k > 0);
-            mma_commit(done);
-        }
-    }
-    // O (+)= P V of the V tile in stage ST; arrives on `done`.
-    template <int G, int ST, uint32_t P, bool IN_S> __device__ __forceinline__ void output(bool add, uint64_t *done) const {
-        extern __shared__ __align__(1024) uint8_t dyn[];
-        constexpr uint32_t idesc = mma_idesc(128, PA_D, true);
-        tc_fence_after();
-        if (leader) {
-            const uint64_t d = smem_desc(smem_addr(dyn) + (2 + ST) * TILE_BYTES, TILE_BYTES / 2, 1024);
-#pragma unroll
-            for (int k = 0; k < PA_TILE / 16; ++k)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    mma_ts(TM::o(G), P + (IN_S ? p_col_in_s(k) : p_col<NT>(k, t)), d + k * 128, idesc,
-                           k || t ? 1u : (uint32_t)add);
-            mma_commit(done);
-        }
-    }
+// Steps are tiles (buffer = stage) or, for two groups, half tiles (buffer =
+// half).  Each step of a group goes scores -> softmax -> P V; where P replaces
+// S, the next scores in that buffer wait for P V.  A wait or an arrival costs
+// a thread some 100 clocks, so the two products have a thread each, and one
+// copy of code serves every stage, buffer and group (instruction fetch, too,
+// is a limit of a kernel with so many roles).
+struct Operands {
+    static constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);    // descriptor: sbo, version, swizzle
+    uint32_t k_lo, v_lo;
+    __device__ __forceinline__ Operands(uint32_t tiles)
+        : k_lo((tiles >> 4) | (1u << 16)), v_lo(((tiles + 2 * TILE_BYTES) >> 4) | ((TILE_BYTES / 2 / 16) << 16)) {}
 };
 
-__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(FULL, mbar_wait(bar, parity));
-}
-
-// The next tile's scores, if there is one, and P V of this tile, for a group
-// with one buffer: P replaces S, so the scores wait for P V.
-template <int MT, int NT, int G, int ST>
-__device__ __forceinline__ bool pair_scores(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t ph) {
-    if (!all_wait(&sh.k_full[ST], (tile >> 1) & 1)) return false;
-    if (!all_wait(&sh.p_empty[G][0], (ph & 1) ^ 1)) return false;
-    pr.template scores<G, ST, Tmem<MT, NT>::half(G, 0)>(&sh.s_full[G][0]);
-    if (pr.leader) mma_commit(&sh.k_empty[ST]);
-    return true;
-}
-template <int MT, int NT, int G, int ST>
-__device__ __forceinline__ bool pair_output(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t &ph, bool add) {
-    if (!all_wait(&sh.v_full[ST], (tile >> 1) & 1)) return false;
-    if (!all_wait(&sh.p_full[G][0], ph & 1)) return false;
-    pr.template output<G, ST, Tmem<MT, NT>::half(G, 0), true>(add, &sh.p_empty[G][0]);
-    if (pr.leader) mma_commit(&sh.v_empty[ST]);
-    ph ^= 1u;
-    return true;
-}
-// The same for one group with two buffers of S and P (buffer = stage).
-template <int MT, int NT, int ST>
-__device__ __forceinline__ bool tile_scores(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t ph) {
-    if (!all_wait(&sh.k_full[ST], (tile >> 1) & 1)) return false;
-    if (!all_wait(&sh.s_empty[0][ST], ((ph >> ST) & 1) ^ 1)) return false;
-    pr.template scores<0, ST, Tmem<MT, NT>::s(ST)>(&sh.s_full[0][ST]);
-    if (pr.leader) mma_commit(&sh.k_empty[ST]);
-    return true;
-}
-template <int MT, int NT, int ST>
-__device__ __forceinline__ bool tile_output(const Products<MT, NT> &pr, Shared<MT> &sh, int tile, uint32_t &ph, bool add) {
-    if (!all_wait(&sh.v_full[ST], (tile >> 1) & 1)) return false;
-    if (!all_wait(&sh.p_full[0][ST], (ph >> ST) & 1)) return false;
-    pr.template output<0, ST, Tmem<MT, NT>::p(ST), false>(add, &sh.p_empty[0][ST]);
-    if (pr.leader) mma_commit(&sh.v_empty[ST]);
-    ph ^= 1u << ST;
-    return true;
-}
-
-// One warp for each group G of rows.  Every warp takes part in every tile: a
-// stage is free when all of them have let go of it.
-template <int MT, int NT, int G>
-__device__ __forceinline__ bool issue_products(const PagedAttnArgs &a, Shared<MT> &sh, bool leader) {
-    const Products<MT, NT> pr = {leader};
+template <int MT, int NT>
+__device__ __forceinline__ bool issue_scores(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles) {
+    using TM = Tmem<MT, NT>;
+    const Operands op(tiles);
     Cursor c = sh.start;
     int no = 0;                               // tiles so far: stage no % 2, phase no / 2
-    uint32_t ph = 0, pq = 0;                  // phases of the group's two buffers, and of q_full
-    while (__shfl_sync(FULL, c.left > 0, 0)) {
-        const int n = __shfl_sync(FULL, c.piece(), 0);
+    uint32_t ph = 0, pq = 0;                  // phases of the groups' two buffers (bit 2 g + b), and of q_full
+    while (c.left > 0) {
+        const int n = c.piece();
         const Rows<MT> rows(a, c);
-        const bool mine = __shfl_sync(FULL, G < rows.groups(), 0), rep = __shfl_sync(FULL, rows.rep, 0);
-        if (mine) {
-            if (!all_wait(&sh.q_full[G], pq)) return false;
-            pq ^= 1u;
+        const int groups = rows.groups();
+        const bool two = MT == 1 || rows.rep;
+        for (int g = 0; g < groups; ++g) {
+            if (!mbar_wait(&sh.q_full[g], (pq >> g) & 1)) return false;
+            pq ^= 1u << g;
         }
-        if (!mine) {
-            for (int t = no; t < no + n; ++t) {
-                if (!all_wait(&sh.k_full[t & 1], (t >> 1) & 1)) return false;
-                if (leader) mbar_arrive(&sh.k_empty[t & 1]);
-                if (!all_wait(&sh.v_full[t & 1], (t >> 1) & 1)) return false;
-                if (leader) mbar_arrive(&sh.v_empty[t & 1]);
+        const uint32_t idesc = two ? mma_idesc(128, PA_TILE, false) : mma_idesc(128, PA_TILE / 2, false);
+        const int steps = two ? 1 : 2 * groups;               // of a tile: half, then group
+        for (const int end = no + n; no < end; ++no) {
+            const int st = no & 1;
+            if (!mbar_wait(&sh.k_full[st], (no >> 1) & 1)) return false;
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
+                const int h = i >= groups ? 1 : 0, g = i - h * groups, b = two ? st : h;
+                if (!mbar_wait(two ? &sh.s_empty[g][b] : &sh.p_empty[g][b], ((ph >> (2 * g + b)) & 1) ^ 1)) return false;
+                ph ^= 1u << (2 * g + b);
+                tc_fence_after();
+                const uint32_t d = two ? TM::s(b) : TM::half(g, h), q = TM::q(g);
+                const uint32_t lo = op.k_lo + st * (TILE_BYTES >> 4) + h * (32 * 128 / 16);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)   // 32 bytes of a row; the second 64 elements in the next block
+                    mma_ts(d, q + k * 8, lo + (k >> 2) * (TILE_BYTES / 2 / 16) + (k & 3) * 2, op.HI, idesc, k > 0);
+                mma_commit(&sh.s_full[g][b]);
             }
-        } else if (G == 0 && (MT == 1 || rep)) {
-            // scores of tile i before P V of tile i - 1
-            uint32_t f = ph;                  // phases as the scores see them, a tile ahead
-            for (int i = 0; i <= n; ++i) {
-                const int t = no + i;
-                if (i < n) {
-                    if (!(t & 1 ? tile_scores<MT, NT, 1>(pr, sh, t, f) : tile_scores<MT, NT, 0>(pr, sh, t, f))) return false;
-                    f ^= 1u << (t & 1);
+            mma_commit(&sh.k_empty[st]);
+        }
+        c.skip(a, n);
+    }
+    return true;
+}
+
+template <int MT, int NT>
+__device__ __forceinline__ bool issue_outputs(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles) {
+    using TM = Tmem<MT, NT>;
+    constexpr uint32_t idesc = mma_idesc(128, PA_D, true);
+    const Operands op(tiles);
+    Cursor c = sh.start;
+    int no = 0;
+    uint32_t ph = 0;
+    while (c.left > 0) {
+        const int n = c.piece();
+        const Rows<MT> rows(a, c);
+        const int groups = rows.groups();
+        const bool two = MT == 1 || rows.rep;
+        const int steps = two ? 1 : 2 * groups;
+        uint32_t add = 0;                     // bit g: O of the group holds earlier steps
+        for (const int end = no + n; no < end; ++no) {
+            const int st = no & 1;
+            if (!mbar_wait(&sh.v_full[st], (no >> 1) & 1)) return false;
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
+                const int h = i >= groups ? 1 : 0, g = i - h * groups, b = two ? st : h;
+                if (!mbar_wait(&sh.p_full[g][b], (ph >> (2 * g + b)) & 1)) return false;
+                ph ^= 1u << (2 * g + b);
+                tc_fence_after();
+                const uint32_t o = TM::o(g), pc = two ? TM::p(b) : TM::half(g, h);
+                const uint32_t lo = op.v_lo + st * (TILE_BYTES >> 4) + h * (32 * 128 / 16);
+#pragma unroll
+                for (int k = 0; k < PA_TILE / 16; ++k) {
+                    if (k == 2 && !two) break;
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        mma_ts(o, pc + p_col<NT>(k, x), lo + k * 128, op.HI, idesc, k || x ? 1u : (add >> g) & 1u);
                 }
-                if (i > 0 && !(t & 1 ? tile_output<MT, NT, 0>(pr, sh, t - 1, ph, i > 1)
-                                     : tile_output<MT, NT, 1>(pr, sh, t - 1, ph, i > 1)))
-                    return false;
+                add |= 1u << g;
+                mma_commit(&sh.p_empty[g][b]);
             }
-        } else if (MT == 2) {
-            for (int i = 0; i <= n; ++i) {
-                const int t = no + i;
-                if (i > 0 && !(t & 1 ? pair_output<MT, NT, G, 0>(pr, sh, t - 1, ph, i > 1)
-                                     : pair_output<MT, NT, G, 1>(pr, sh, t - 1, ph, i > 1)))
-                    return false;
-                if (i < n && !(t & 1 ? pair_scores<MT, NT, G, 1>(pr, sh, t, ph) : pair_scores<MT, NT, G, 0>(pr, sh, t, ph)))
-                    return false;
-            }
+            mma_commit(&sh.v_empty[st]);
         }
-        no += n;
         c.skip(a, n);
     }
     return true;
@@ -844,39 +819,27 @@ template <int MT, int NT> struct Softmax {
         ph ^= 1u << b;
         return true;
     }
-    // A row per thread, two groups: the piece's tile i, its weights in the place of its scores.
-    __device__ __forceinline__ bool tile_pair(int i, const uint2 &valid) {
-        if (!mbar_wait(&sh.s_full[g][0], ph & 1)) return false;
+    // A row per thread, two groups: half h of a tile, its weights in the place of its scores.
+    __device__ __forceinline__ bool half_tile(bool first, int h, const uint32_t &valid) {
+        if (!mbar_wait(&sh.s_full[g][h], (ph >> h) & 1)) return false;
         tc_fence_after();
-        const uint2 mask = valid;
-        const uint32_t ts = lanes + TM::half(g, 0);
+        const uint32_t mask = valid, ts = lanes + TM::half(g, h);
         uint32_t s[32];
-        float mt = -INFINITY;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            tmem_ld32(ts + 32 * h, s);
-            tmem_wait_ld();
-            const uint32_t w = h ? mask.y : mask.x;
-            if (w != FULL) hide(s, w);
-            mt = fmaxf(mt, row_max<32>(s));
-        }
-        // (the scores were issued after the products before them had ended)
-        if (!rescale(mt, i > 0 ? &sh.p_empty[g][0] : nullptr, (ph & 1) ^ 1)) return false;
+        tmem_ld32(ts, s);
+        tmem_wait_ld();
+        if (mask != FULL) hide(s, mask);
+        if (!rescale(row_max<32>(s), first ? nullptr : &sh.p_empty[g][h ^ 1], ((ph >> (h ^ 1)) & 1) ^ 1)) return false;
         const float rf = ref == -INFINITY ? 0.f : ref;
-#pragma unroll 1
-        for (int h = 1; h >= 0; --h) {        // (the second half's scores are still there)
-            put(s, rf, ts + 32 * h);
-            put(s + 16, rf, ts + 32 * h + 8);
-            if (h) {
-                tmem_ld32(ts, s);
-                tmem_wait_ld();
-                if (mask.x != FULL) hide(s, mask.x);
-            }
-        }
+        put(s, rf, ts);
+        put(s + 16, rf, ts + 8);
         tmem_wait_st();
-        arrive(&sh.s_empty[g][0]);            // (for the replicated pieces, which wait for it)
-        arrive(&sh.p_full[g][0]);
-        ph ^= 1u;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh.s_empty[g][h]);   // (for the replicated pieces, which wait for it)
+            mbar_arrive(&sh.p_full[g][h]);
+        }
+        ph ^= 1u << h;
         return true;
     }
 };
@@ -943,11 +906,13 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             for (int i = 0; i < n; ++i)
                 if (!sm.tile_full(i, (t0 + i) & 1, sh.mask[(t0 + i) % MASK_RING])) return false;
         } else {
-            for (int i = 0; i < n; ++i)
-                if (!sm.tile_pair(i, sh.mask[(t0 + i) % MASK_RING])) return false;
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i)
+                if (!sm.half_tile(i == 0, i & 1, reinterpret_cast<const uint32_t *>(sh.mask)[(2 * t0 + i) % (2 * MASK_RING)]))
+                    return false;
         }
         // the piece's partial
-        const int lb = MT == 1 || rows.rep ? (no - 1) & 1 : 0;
+        const int lb = MT == 1 || rows.rep ? (no - 1) & 1 : 1;
         if (!mbar_wait(&sh.p_empty[g][lb], ((sm.ph >> lb) & 1) ^ 1)) return false;
         tc_fence_after();
         const int seg = pre ? at.head * a.row_tiles + at.seg : at.head * a.B + at.seg - a.row_tiles;
@@ -976,17 +941,6 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     return true;
 }
 
-// Warps: 4 MT softmax, 16 producers, 4 - MT scouts, MT for the products.  The
-// block is launched with REGS a thread, and each group of four warps takes what it
-// needs of their sum.
-template <int MT> struct Roles {
-    static constexpr int SCOUT = 4 * MT + PROD_WARPS, PRODUCTS = SCOUT + 4 - MT;
-    static constexpr int THREADS = (PRODUCTS + MT) * 32;
-    static constexpr int REGS = MT == 1 ? 80 : 72;
-    static constexpr int SOFTMAX = MT == 1 ? 128 : 80, PRODUCER = 72, REST = MT == 1 ? 64 : 56;
-    static_assert(REGS * THREADS <= 65536, "registers of an SM");
-    static_assert(128 * MT * SOFTMAX + 32 * PROD_WARPS * PRODUCER + 128 * REST <= REGS * THREADS, "register shares");
-};
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -1004,8 +958,8 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh.k_full[i], PROD_WARPS / 4);
                 mbar_init(&sh.v_full[i], PROD_WARPS / 4);
-                mbar_init(&sh.k_empty[i], MT);
-                mbar_init(&sh.v_empty[i], MT);
+                mbar_init(&sh.k_empty[i], 1);
+                mbar_init(&sh.v_empty[i], 1);
             }
             for (int g = 0; g < MT; ++g) {
                 mbar_init(&sh.q_full[g], 4);
@@ -1022,7 +976,8 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
             }
             mbar_init(&sh.pair_done, 4);
             mbar_init(&sh.heads, PROD_WARPS);
-            mbar_init(&sh.drain, MT);
+            mbar_init(&sh.drain[0], 1);
+            mbar_init(&sh.drain[1], 1);
             mbar_init_fence();
         }
     }
@@ -1086,11 +1041,13 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         if (warp < PRODUCTS) {
             ok = scout<MT>(a, sh, warp - SCOUT, lane);
         } else {
-            const bool leader = elect_one();
-            ok = sh.tmem == 0u && (warp == PRODUCTS ? issue_products<MT, NT, 0>(a, sh, leader)
-                                                    : issue_products<MT, NT, MT - 1>(a, sh, leader));
-            if (leader) mma_commit(&sh.drain);    // nothing may be in flight when tensor memory goes
-            if (!mbar_wait(&sh.drain, 0)) ok = false;
+            if (elect_one()) {
+                ok = sh.tmem == 0u && (warp == PRODUCTS ? issue_scores<MT, NT>(a, sh, tiles)
+                                                        : issue_outputs<MT, NT>(a, sh, tiles));
+                mma_commit(&sh.drain[warp - PRODUCTS]);       // nothing may be in flight when tensor memory goes
+                if (!mbar_wait(&sh.drain[warp - PRODUCTS], 0)) ok = false;
+            }
+            __syncwarp();
         }
     }
     if (!ok) sh.failed = 1;
