@@ -25,9 +25,10 @@ namespace hqmq {
 constexpr int PW_LOOP_WARPS = 4, PW_TABLE_WARPS = 8;
 constexpr int PW_TOKENS = 8;                  // tokens a warp of the table kernel holds
 constexpr int PW_COPIES = 4;                  // of the codeword table
-constexpr int PW_BATCH = 4;                   // of them, tokens whose records are in flight
+constexpr int PW_BATCH = 2;                   // of them, tokens whose records are in flight
 constexpr int PW_SEARCH_FROM = 8;             // tokens of a sequence, on average
 constexpr uint32_t PW_SEARCH_S = 12;
+constexpr int PW_RUNS_FROM = 4;               // tokens of a sequence, on average
 
 struct WriteArgs {
     PagesDev p[2];
@@ -455,8 +456,10 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(co
     n.add_to(a.st_out, lane);
 }
 
-template <int DT, int BB>
-__global__ void __launch_bounds__(PW_LOOP_WARPS * 32, 8) k_paged_write_loop(const __grid_constant__ WriteArgs a) {
+// CTAS: resident on an SM.  Steps of one token want many short CTAs (64 sequences, 8 heads: 8.0 us at 7, 10.2
+// at 5), longer runs the registers for more chunks' arithmetic at once (runs of 16, S = 8: 14.6 and 11.5 us).
+template <int DT, int BB, int CTAS>
+__global__ void __launch_bounds__(PW_LOOP_WARPS * 32, CTAS) k_paged_write_loop(const __grid_constant__ WriteArgs a) {
     constexpr int WARPS = PW_LOOP_WARPS, THREADS = WARPS * 32;
     __shared__ float4 s_cb[PG_MAX_S];
     __shared__ uint32_t s_cnt[WARPS];
@@ -528,6 +531,17 @@ __global__ void __launch_bounds__(PW_LOOP_WARPS * 32, 8) k_paged_write_loop(cons
     n.add_to(a.st_out, lane);
 }
 
+using WriteKernel = void (*)(WriteArgs);
+template <int DT, int BB> WriteKernel write_kernel_b(bool search, bool runs_of_some) {
+    return search ? k_paged_write_table<DT, BB> : runs_of_some ? k_paged_write_loop<DT, BB, 5> : k_paged_write_loop<DT, BB, 7>;
+}
+// bb: bits of the indices of K and V, where compiled for (S = 6 .. 10 and 22 .. 42), else 0.
+template <int DT> WriteKernel write_kernel(uint32_t bb, bool search, bool runs_of_some) {
+    return bb == 8    ? write_kernel_b<DT, 8>(search, runs_of_some)
+           : bb == 10 ? write_kernel_b<DT, 10>(search, runs_of_some)
+                      : write_kernel_b<DT, 0>(search, runs_of_some);
+}
+
 }  // namespace hqmq
 
 extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pages *v,
@@ -562,22 +576,17 @@ extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pag
     const int roles = v ? 2 : 1;
     const uint32_t S = v && v->S > k->S ? v->S : k->S;
     // the tables pay for runs of some tokens (their codewords have to be brought to shared memory) and
-    // codebooks of some size (the loop costs about 25 instructions a secondary, the table 250 in all)
+    // codebooks of some size (the loop costs about 25 instructions a secondary, the table 250 in all:
+    // 7 sequences of up to 301 tokens, S = 8: 11.5 us by the loop, 35 by the tables; 4096 tokens, S = 32: 131 and 61)
     const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs && S >= PW_SEARCH_S;
     const size_t smem = search ? (size_t)(24 * S + 1) * PW_COPIES * sizeof(float4) : 0;
     // with tables a CTA goes through runs of 64 tokens or more
     const int64_t gx = search && k->page_size < 64 ? (runs * k->page_size + 63) / 64 : runs;
     const dim3 grid((unsigned)gx, (unsigned)k->heads, (unsigned)roles);
     const uint32_t bb = v && bv != bk ? 0 : bk;
-    auto kern = dtype == HQMQ_BF16
-        ? (search ? (bb == 8 ? k_paged_write_table<HQMQ_BF16, 8> : bb == 10 ? k_paged_write_table<HQMQ_BF16, 10>
-                                                                            : k_paged_write_table<HQMQ_BF16, 0>)
-                  : (bb == 8 ? k_paged_write_loop<HQMQ_BF16, 8> : bb == 10 ? k_paged_write_loop<HQMQ_BF16, 10>
-                                                                           : k_paged_write_loop<HQMQ_BF16, 0>))
-        : (search ? (bb == 8 ? k_paged_write_table<HQMQ_F32, 8> : bb == 10 ? k_paged_write_table<HQMQ_F32, 10>
-                                                                           : k_paged_write_table<HQMQ_F32, 0>)
-                  : (bb == 8 ? k_paged_write_loop<HQMQ_F32, 8> : bb == 10 ? k_paged_write_loop<HQMQ_F32, 10>
-                                                                          : k_paged_write_loop<HQMQ_F32, 0>));
+    const bool runs_of_some = n_tokens >= PW_RUNS_FROM * n_seqs;
+    auto kern = dtype == HQMQ_BF16 ? write_kernel<HQMQ_BF16>(bb, search, runs_of_some)
+                                   : write_kernel<HQMQ_F32>(bb, search, runs_of_some);
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
