@@ -89,13 +89,20 @@ template <> struct Raw8<float> {
 };
 
 // A CTA takes a span of tokens and blockDim.x / LPV heads (blockIdx.y: which);
-// a thread stays with its 16 elements of its head, so the weights stay in
-// registers, and walks the tokens, loading the next one's elements before it
-// works on the current one's.
+// a thread stays with its 16 elements of its head and walks the tokens, loading
+// the next one's elements before it works on the current one's.
+// Bandwidth is the bound, so what counts is loads in flight: weights and
+// angles come from shared memory, which leaves 64 registers a thread, and the
+// span is chosen so that the last round of CTAs is nearly full (8192 tokens of
+// 40 heads of 128, bf16, 168 MB: 31 us, 5.4 TB/s; weights in registers and
+// spans of 8: 41 us).
 template <typename E, int LPV, bool PAIRS>
-__global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const __grid_constant__ NormRopeArgs a, unsigned tokens,
-                                                          int span) {
+__global__ void __launch_bounds__(NR_THREADS, 2) k_norm_rope(const __grid_constant__ NormRopeArgs a, unsigned tokens,
+                                                             int span) {
+    // A part's eight angles, and its 16 weights, as four float4 each that lie LPV (of those that rotate: R / 16)
+    // apart: neighbouring lanes read neighbouring words.
     __shared__ __align__(16) float2 s_cs[NR_MAX_ANGLES];
+    __shared__ __align__(16) float4 s_w[2][4 * LPV];
     pdl_wait();
     pdl_trigger();
     const unsigned t0 = blockIdx.x * span;
@@ -121,25 +128,36 @@ __global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const __grid_constant_
         r0.load(in + e0);
         r1.load(in + e1);
     }
-    float g[16];
-    if (on && w) {
-        if (a.w_f32) {
-            Raw8<float> q;
-            q.load(reinterpret_cast<const float *>(w) + e0);
-            q.get(g);
-            q.load(reinterpret_cast<const float *>(w) + e1);
-            q.get(g + 8);
-        } else {
-            Raw8<__nv_bfloat16> q;
-            q.load(reinterpret_cast<const __nv_bfloat16 *>(w) + e0);
-            q.get(g);
-            q.load(reinterpret_cast<const __nv_bfloat16 *>(w) + e1);
-            q.get(g + 8);
-        }
+    // (all these loads are on their way before the first is waited for)
+    const int angles = n_tok * half;
+    int pos = 0;
+    double freq = 0.0;
+    if ((int)threadIdx.x < angles) {
+        const int k = threadIdx.x / half;
+        pos = a.pos[t0 + k];
+        freq = a.inv_freq[threadIdx.x - k * half];
     }
-    for (int i = threadIdx.x; i < n_tok * half; i += blockDim.x) {
-        const int k = i / half;
-        s_cs[i] = angle_cs(a.pos[t0 + k], a.inv_freq[i - k * half]);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+        const int side = i >= a.D, e = i - side * a.D;
+        // element e is number m of part p
+        const bool er = e < a.R && !PAIRS, up = er && e >= half;
+        const int p = er ? (up ? e - half : e) >> 3 : e >> 4, m = er ? (e & 7) + (up ? 8 : 0) : e & 15;
+        const void *sw = a.w[side];
+        if (sw)
+            reinterpret_cast<float *>(s_w[side])[((m >> 2) * LPV + p) * 4 + (m & 3)] =
+                a.w_f32 ? reinterpret_cast<const float *>(sw)[e]
+                        : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(sw)[e]);
+    }
+    const int rot_parts = half / 8;
+    for (int i = threadIdx.x; i < angles;) {
+        const int k = i / half, j = i - k * half;
+        s_cs[k * half + ((((j >> 1) & 3) * rot_parts + (j >> 3)) << 1) + (j & 1)] = angle_cs(pos, freq);
+        i += blockDim.x;
+        if (i < angles) {
+            pos = a.pos[t0 + i / half];
+            freq = a.inv_freq[i % half];
+        }
     }
     __syncthreads();
     const float inv_d = 1.0f / (float)a.D;
@@ -173,13 +191,19 @@ __global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const __grid_constant_
         if (w) {
             const float r = rsqrtf(sum * inv_d + a.eps);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = f[i] * r * g[i];
+            for (int i = 0; i < 16; i += 4) {
+                const float4 g = s_w[is_k][(i >> 2) * LPV + part];
+                f[i] = f[i] * r * g.x;
+                f[i + 1] = f[i + 1] * r * g.y;
+                f[i + 2] = f[i + 2] * r * g.z;
+                f[i + 3] = f[i + 3] * r * g.w;
+            }
         }
         if (rot) {
-            const float4 *cs = reinterpret_cast<const float4 *>(s_cs + k * half + part * 8);
+            const float4 *cs = reinterpret_cast<const float4 *>(s_cs + k * half) + part;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float4 c = cs[i / 2];       // pairs i and i + 1
+                const float4 c = cs[i / 2 * rot_parts];       // pairs i and i + 1
                 constexpr int V = PAIRS ? 1 : 8, U = PAIRS ? 2 : 1;
                 const float p = f[i * U], q = f[i * U + V], r = f[(i + 1) * U], t = f[(i + 1) * U + V];
                 f[i * U] = p * c.x - q * c.y;
@@ -244,14 +268,23 @@ __global__ void __launch_bounds__(NR_ANY_WARPS * 32) k_norm_rope_any(NormRopeArg
 
 template <typename E, int LPV>
 static cudaError_t launch_norm_rope_lpv(const NormRopeArgs &a, unsigned tokens, cudaStream_t stream) {
-    // tokens of a CTA: up to 8 (their angles fit shared memory), so that the angles' latency is paid once
-    // for all of them, fewer where that would leave SMs idle
-    int span = 8;
-    while (span > 1 && (span * (a.R / 2) > NR_MAX_ANGLES || tokens / span < 4 * 148)) span /= 2;
     // heads: all in one CTA if they fit, in equal shares otherwise; a few tokens spread theirs over the SMs
     const int total = a.heads[0] + a.heads[1], most = (tokens < 148 ? 128 : NR_THREADS) / LPV;
     const int shares = (total + most - 1) / most, heads = (total + shares - 1) / shares;
-    const dim3 g((tokens + span - 1) / span, shares), b((heads * LPV + 31) / 32 * 32);
+    const int threads = (heads * LPV + 31) / 32 * 32;
+    // tokens of a CTA (their angles fit shared memory): the fewest rounds of resident CTAs (64 registers a
+    // thread), each as long as its tokens and a start that is worth about two
+    const int64_t slots = 148 * (int64_t)(1024 / threads);
+    int span = 1;
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= 16 && n * (a.R / 2) <= NR_MAX_ANGLES; ++n) {
+        const int64_t ctas = (int64_t)((tokens + n - 1) / n) * shares, cost = (ctas + slots - 1) / slots * (n + 2);
+        if (cost < best) {
+            best = cost;
+            span = n;
+        }
+    }
+    const dim3 g((tokens + span - 1) / span, shares), b(threads);
     return a.interleaved ? launch_pdl(k_norm_rope<E, LPV, true>, g, b, 0, stream, a, tokens, span)
                          : launch_pdl(k_norm_rope<E, LPV, false>, g, b, 0, stream, a, tokens, span);
 }
