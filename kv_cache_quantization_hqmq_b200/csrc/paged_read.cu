@@ -6,13 +6,15 @@
 // anew with every page), then each warp decodes its tokens, a lane two chunks
 // (bf16) or one (fp32), so that every store is 16 bytes and a token's row is
 // contiguous.  The loads of several steps are issued before the first is used.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace hqmq {
 
 constexpr int PR_WARPS = 8;
 constexpr int PR_THREADS = PR_WARPS * 32;
-constexpr int PR_COPIES = 4;                  // of the codeword table: bank conflicts in pairs only
+constexpr int PR_COPIES = 2;                  // of the codeword table
 
 struct ReadArgs {
     PagesDev p;
@@ -22,10 +24,13 @@ struct ReadArgs {
     DevStatus *st;
 };
 
-struct ReadTok {
-    long long page;                           // page * heads + head, < 0: leave the row
+// A token, ready for its decoders: no address arithmetic is left to them.
+struct __align__(16) ReadTok {
+    const uint32_t *words;                    // (of some row, if this one is left alone)
+    const uint16_t *radius;
+    const uint2 *val;                         // its first value
     uint32_t flags;
-    int slot;
+    int left;                                 // slots of the page from there; < 0: the row is left alone
 };
 
 __device__ __forceinline__ float4 half4(uint2 h) {
@@ -34,7 +39,8 @@ __device__ __forceinline__ float4 half4(uint2 h) {
 }
 
 // CPL: chunks a lane takes (2: bf16, 1: fp32); a warp's step covers CPL tokens.
-template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(ReadArgs a) {
+// BB: bits of an index, if known to the compiler.
+template <int CPL, int BB> __global__ void __launch_bounds__(PR_THREADS, 4) k_paged_read(ReadArgs a) {
     extern __shared__ float4 s_tab[];         // [24 S + 1][PR_COPIES]
     __shared__ ReadTok s_tok[PR_THREADS];
     __shared__ uint32_t s_sum[PR_WARPS];
@@ -48,7 +54,7 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
 
     // this thread's token: its page, flags and the slot of its first value
     const int me = t0 + threadIdx.x;
-    ReadTok tok = {-1, 0u, 0};
+    ReadTok tok = {p.words, p.radius, nullptr, 0u, -1};
     int page = -1;
     if ((int)threadIdx.x < n) {
         const int col = me >> p.page_shift;
@@ -56,11 +62,15 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
         if (page < 0 || page >= p.n_pages) {
             page = -1;
             if (a.st) atomicOr(&a.st->flags, HQMQ_FLAG_BAD_PAGE);
-        } else {
-            tok.page = (long long)page * p.heads + head;
         }
     }
     const int row = me & (p.page_size - 1);
+    if (page >= 0) {
+        const size_t at = p.at(page, head, row);
+        tok.words = p.words + at * p.b;
+        tok.radius = p.radius + at * PG_CHUNKS;
+        tok.left = 0;
+    }
     if (p.flags) {
         uint32_t before = 0;                  // flagged chunks in the rows of the first page before t0
         if (page >= 0) tok.flags = p.flags[p.at(page, head, row)];
@@ -86,7 +96,10 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
         __syncthreads();
         for (int w = max(first, 0) >> 5; w < warp; ++w) start += s_sum[w];
         if (first < 0) start += before;
-        tok.slot = (int)start;
+        if (page >= 0) {
+            tok.left = max(p.cap - (int)start, 0);
+            tok.val = reinterpret_cast<const uint2 *>(p.slots(page, head)) + start;
+        }
     }
     s_tok[threadIdx.x] = tok;
     const uint32_t words = 24u * p.S;
@@ -99,42 +112,44 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
     __syncthreads();
 
     constexpr int STEPS = 4;                  // loads in flight: STEPS tokens a lane
+    const uint32_t b = BB ? BB : p.b;
     const int sub = CPL == 2 ? lane >> 4 : 0, c0 = CPL == 2 ? 2 * (lane & 15) : lane;
-    const uint32_t bit = (uint32_t)c0 * p.b, wi = bit >> 5, sh = bit & 31u, mask = (1u << p.b) - 1u;
+    const uint32_t bit = (uint32_t)c0 * b, wi = bit >> 5, sh = bit & 31u, mask = (1u << b) - 1u;
+    const bool two = wi + 1 < b;              // (CPL b bits lie in one or two words: b <= 11)
+    const uint32_t below = (1u << c0) - 1u;
     const float4 *tab = s_tab + (lane & (PR_COPIES - 1));
+    using Out = typename std::conditional<CPL == 2, uint16_t, float>::type;
+    Out *const y0 = reinterpret_cast<Out *>(a.y) + (((size_t)seq * p.heads + head) * a.T + t0 + sub) * 128 + 4 * c0;
     bool bad = false;
     for (int i0 = warp * STEPS * CPL; i0 < n; i0 += PR_WARPS * STEPS * CPL) {
-        uint32_t lo[STEPS], hi[STEPS], rad[STEPS];
-        uint2 val[STEPS];
-        ReadTok k[STEPS];
+        uint32_t lo[STEPS], hi[STEPS], rad[STEPS], own[STEPS];       // own: which of the lane's chunks have values
+        uint2 val[STEPS];                     // the first of them
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int i = i0 + s * CPL + sub;
-            k[s].page = -1;
-            if (i < n) k[s] = s_tok[i];
-            lo[s] = hi[s] = rad[s] = 0u;
-            if (k[s].page < 0) continue;
-            const size_t at = ((size_t)k[s].page << p.page_shift) + ((t0 + i) & (p.page_size - 1));
-            const uint32_t *w = p.words + at * p.b;
-            lo[s] = __ldcs(w + wi);
-            hi[s] = wi + 1 < p.b ? __ldcs(w + wi + 1) : 0u;
-            if (CPL == 2) rad[s] = __ldcs(reinterpret_cast<const uint32_t *>(p.radius + at * PG_CHUNKS) + (lane & 15));
-            else rad[s] = p.radius[at * PG_CHUNKS + lane];
-            k[s].slot += __popc(k[s].flags & ((1u << c0) - 1u));
-            k[s].flags = (k[s].flags >> c0) & (CPL == 2 ? 3u : 1u);
-            if (k[s].flags && k[s].slot < p.cap)
-                val[s] = __ldcs(reinterpret_cast<const uint2 *>(p.val) + (size_t)k[s].page * p.cap + k[s].slot);
+            const ReadTok &k = s_tok[i0 + s * CPL + sub];
+            const uint32_t *w = k.words + wi;
+            lo[s] = __ldcs(w);
+            hi[s] = two ? __ldcs(w + 1) : 0u;
+            if (CPL == 2) rad[s] = __ldcs(reinterpret_cast<const uint32_t *>(k.radius + c0));
+            else rad[s] = __ldcs(k.radius + c0);
         }
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            if (k[s].page < 0) continue;
-            const int i = i0 + s * CPL + sub;
-            // CPL b bits: one or two words (b <= 11)
+            const ReadTok &k = s_tok[i0 + s * CPL + sub];
+            const uint32_t flags = k.flags;
+            const int room = k.left - __popc(flags & below);         // slots from the lane's first value
+            own[s] = room <= 0 ? 0u : (flags >> c0) & (CPL == 2 ? 3u : 1u);
+            if (CPL == 2 && room == 1 && own[s] == 3u) own[s] = 1u;
+            if (own[s]) val[s] = __ldcs(k.val + __popc(flags & below));
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (s_tok[i0 + s * CPL + sub].left < 0) continue;
             const uint32_t v = __funnelshift_r(lo[s], hi[s], sh);
             float4 y[CPL];
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                const uint32_t idx = (v >> (c * p.b)) & mask;
+                const uint32_t idx = (v >> (c * b)) & mask;
                 const float r = f16_bits_to_f32(c ? rad[s] >> 16 : rad[s] & 0xFFFFu);
                 const float4 w = tab[min(idx, words) * PR_COPIES];
                 y[c] = make_float4(__fmul_rn(r, w.x), __fmul_rn(r, w.y), __fmul_rn(r, w.z), __fmul_rn(r, w.w));
@@ -143,13 +158,14 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
                     bad = true;
                 }
             }
-            if (k[s].flags && k[s].slot < p.cap) {
-                y[CPL == 2 && !(k[s].flags & 1u) ? CPL - 1 : 0] = half4(val[s]);
-                if (CPL == 2 && k[s].flags == 3u && k[s].slot + 1 < p.cap)
-                    y[CPL - 1] = half4(__ldcs(reinterpret_cast<const uint2 *>(p.val) + (size_t)k[s].page * p.cap +
-                                              k[s].slot + 1));
+            if (own[s]) {
+                y[CPL == 2 && own[s] == 2u ? CPL - 1 : 0] = half4(val[s]);
+                if (CPL == 2 && own[s] == 3u) {
+                    const ReadTok &k = s_tok[i0 + s * CPL + sub];
+                    y[CPL - 1] = half4(__ldcs(k.val + __popc(k.flags & below) + 1));
+                }
             }
-            const size_t out = (((size_t)seq * p.heads + head) * a.T + t0 + i) * 128 + 4 * c0;
+            Out *const out = y0 + (i0 + s * CPL) * 128;
             if (CPL == 2) {
                 uint32_t h[4];
 #pragma unroll
@@ -159,9 +175,9 @@ template <int CPL> __global__ void __launch_bounds__(PR_THREADS) k_paged_read(Re
                     h[2 * c] = *reinterpret_cast<const uint32_t *>(&p0);
                     h[2 * c + 1] = *reinterpret_cast<const uint32_t *>(&p1);
                 }
-                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.y) + out) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[2], h[3]);
             } else {
-                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.y) + out) = y[0];
+                *reinterpret_cast<float4 *>(out) = y[0];
             }
         }
     }
@@ -187,7 +203,8 @@ extern "C" int hqmq_launch_paged_read(const hqmq_kv_pages *c, uint32_t b, int n_
     a.span = 256;
     while (a.span > 32 && (int64_t)((T + a.span - 1) / a.span) * c->heads * n_seqs < 2 * 148) a.span /= 2;
     const size_t smem = (size_t)(24 * c->S + 1) * PR_COPIES * sizeof(float4);
-    auto kern = out_dtype == HQMQ_BF16 ? k_paged_read<2> : k_paged_read<1>;
+    auto kern = out_dtype == HQMQ_BF16 ? (b == 8 ? k_paged_read<2, 8> : b == 10 ? k_paged_read<2, 10> : k_paged_read<2, 0>)
+                                       : (b == 8 ? k_paged_read<1, 8> : b == 10 ? k_paged_read<1, 10> : k_paged_read<1, 0>);
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return HQMQ_ERR_CUDA;
