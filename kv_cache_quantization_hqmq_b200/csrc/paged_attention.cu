@@ -1060,15 +1060,21 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
     if (threadIdx.x == 0 && sh.failed && a.st) atomicOr(&a.st->flags, HQMQ_FLAG_TIMEOUT);
 }
 
-// Joins the partials of every row; one warp per row.
+// Joins the partials of a row, a CTA each.  Its four warps take every fourth
+// partial, four at a time, all of whose loads are issued at once (a lane four
+// elements), and join their four results in shared memory; where the partials
+// are is worked out while the last CTAs of k_paged_attn still run (the lengths
+// were written before that kernel began).  Latency is the bound: 1024 rows of
+// about 16 partials take 4.5 us after the last CTA.
+constexpr int PJ_BATCH = 4;
 template <int MT>
 __global__ void __launch_bounds__(128)
-k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.Hk * a.G) return;
-    const int g = (int)(row % a.G), head = (int)(row / a.G % a.Hk), b = (int)(row / a.G / a.Hk);
+k_paged_join(const __grid_constant__ PagedAttnArgs a, void *o, int out_dtype, float *lse) {
+    __shared__ float s_acc[4][PA_D];
+    __shared__ float2 s_ml[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, rg = (int)((unsigned)row / (unsigned)a.G), g = row - rg * a.G;
+    const int b = (int)((unsigned)rg / (unsigned)a.Hk), head = rg - b * a.Hk;
     int64_t own_total;
     const int64_t before = tiles_before(a, b, &own_total);
     const Shares w(a, own_total);
@@ -1095,49 +1101,59 @@ k_paged_join(PagedAttnArgs a, void *o, int out_dtype, float *lse) {
         own_step = (size_t)a.own_slot_rows * PA_PART;
         own = a.part_own + ((size_t)head * a.B + b + c0) * own_step + g * PA_PART;
     }
+    pdl_wait();
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n_pre + n_own; i0 += 32) {       // a lane looks at one partial
-        const int i = i0 + lane, j = i - n_pre, n = min(32, n_pre + n_own - i0);
-        const float *p = nullptr;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (i < n_pre) p = pre + (size_t)(copies == 4 ? i >> 2 : i) * pre_step + (copies == 4 ? (i & 3) * stride : 0);
-        else if (j < n_own) p = own + (size_t)(j >> 2) * own_step + (j & 3) * a.G * PA_PART;
-        if (p) ml = *reinterpret_cast<const float2 *>(p);
-        float mn = ml.x;
+    for (int i0 = warp; i0 < n_pre + n_own; i0 += 4 * PJ_BATCH) {
+        float2 ml[PJ_BATCH];                  // (-inf: no token, and O may be anything)
+        float4 v[PJ_BATCH];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, o));
-        mn = fmaxf(mn, m);
-        const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);         // (-inf: no token)
-        float sum = ml.x == -INFINITY ? 0.f : ml.y * f;
+        for (int k = 0; k < PJ_BATCH; ++k) {
+            const int i = i0 + 4 * k, j = i - n_pre;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i >= n_pre + n_own) continue;
+            const float *p = j < 0 ? pre + (size_t)(copies == 4 ? i >> 2 : i) * pre_step + (copies == 4 ? (i & 3) * stride : 0)
+                                   : own + (size_t)(j >> 2) * own_step + (j & 3) * a.G * PA_PART;
+            ml[k] = *reinterpret_cast<const float2 *>(p);
+            v[k] = *reinterpret_cast<const float4 *>(p + 4 + 4 * lane);
+        }
+        float mn = m;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        for (int k = 0; k < PJ_BATCH; ++k) mn = fmaxf(mn, ml[k].x);
+        if (mn == -INFINITY) continue;
+        const float f0 = exp2f(m - mn);
         m = mn;
-        l = l * f0 + sum;
+        l *= f0;
         acc.x *= f0; acc.y *= f0; acc.z *= f0; acc.w *= f0;
-        const unsigned there = __ballot_sync(FULL, ml.x != -INFINITY && p != nullptr);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float fk = __shfl_sync(FULL, f, k);
-            const float *pk = reinterpret_cast<const float *>(__shfl_sync(FULL, (unsigned long long)p, k));
-            if (!((there >> k) & 1u)) continue;
-            const float4 v = *reinterpret_cast<const float4 *>(pk + 4 + 4 * lane);
-            acc.x += v.x * fk;
-            acc.y += v.y * fk;
-            acc.z += v.z * fk;
-            acc.w += v.w * fk;
+#pragma unroll
+        for (int k = 0; k < PJ_BATCH; ++k) {
+            if (ml[k].x == -INFINITY) continue;
+            const float f = exp2f(ml[k].x - mn);
+            l += ml[k].y * f;
+            acc.x += v[k].x * f;
+            acc.y += v[k].y * f;
+            acc.z += v[k].z * f;
+            acc.w += v[k].w * f;
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const size_t at = (size_t)row * PA_D + 4 * lane;
-    if (out_dtype == HQMQ_BF16)
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(o) + at) =
-            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-    else
-        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(o) + at) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (lse && lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+    *reinterpret_cast<float4 *>(&s_acc[warp][4 * lane]) = acc;
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    m = fmaxf(fmaxf(s_ml[0].x, s_ml[1].x), fmaxf(s_ml[2].x, s_ml[3].x));
+    l = 0.f;
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (s_ml[k].x == -INFINITY) continue;
+        const float f = exp2f(s_ml[k].x - m);
+        l += s_ml[k].y * f;
+        y += s_acc[k][threadIdx.x] * f;
+    }
+    y = l == 0.f ? 0.f : y * (1.f / l);
+    const size_t at = (size_t)row * PA_D + threadIdx.x;
+    if (out_dtype == HQMQ_BF16) reinterpret_cast<__nv_bfloat16 *>(o)[at] = __float2bfloat16_rn(y);
+    else reinterpret_cast<float *>(o)[at] = y;
+    if (lse && threadIdx.x == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
 }
 
 // Workspace: partials of the prefix's segments, then of the sequences'.  The
@@ -1169,7 +1185,7 @@ static int launch_paged_attn_b(const PagedAttnArgs &a, int ctas, void *o, int ou
     const int64_t rows = (int64_t)a.B * a.Hk * a.G;
     if (ctas > 0 && launch_pdl(kern, dim3(ctas), dim3(Roles<MT>::THREADS), smem, stream, a) != cudaSuccess)
         return HQMQ_ERR_CUDA;
-    return launch_pdl(k_paged_join<MT>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a, o, out_dtype,
+    return launch_pdl(k_paged_join<MT>, dim3((unsigned)rows), dim3(128), 0, stream, a, o, out_dtype,
                       lse) == cudaSuccess
                ? HQMQ_OK : HQMQ_ERR_CUDA;
 }
