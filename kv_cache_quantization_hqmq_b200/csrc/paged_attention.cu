@@ -92,6 +92,11 @@ __device__ __forceinline__ int64_t tiles_before(const PagedAttnArgs &a, int b_en
     return before;
 }
 
+// a / b for a >= 0, b > 0 (a 64-bit division costs some 500 clocks).
+__device__ __forceinline__ int quotient(int64_t a, int64_t b) {
+    return (a | b) < (1ll << 32) ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
 // How the list of all heads' tiles is shared out: CTA c takes the tiles
 // [c len, (c + 1) len).
 struct Shares {
@@ -102,9 +107,7 @@ struct Shares {
         total = per_head * a.Hk;
         len = (uint32_t)max((total + PA_CTAS - 1) / PA_CTAS, (int64_t)1);
     }
-    __device__ __forceinline__ int owner(int64_t tile) const {
-        return tile < (1ll << 32) ? (int)((uint32_t)tile / len) : (int)(tile / len);
-    }
+    __device__ __forceinline__ int owner(int64_t tile) const { return quotient(tile, len); }
 };
 
 // A place in the list: tile `tile` of segment `seg` of `head`.
@@ -518,10 +521,15 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
     const uint32_t tile = tiles + (which ? 2u * TILE_BYTES : 0u) + st * TILE_BYTES;
     uint64_t *full = (which ? sh.v_full : sh.k_full) + st, *empty = (which ? sh.v_empty : sh.k_empty) + st;
     const int total = sh.total, last_head = sh.last_head;
-    int head = sh.start.head - 1, meetings = 0;
+    int head = sh.start.head, meetings = 0;
     uint32_t par = 1;                         // phase of `empty` to wait for
     Slot<BT> x, next;
 
+    // (the first head's tables while the scouts look the first tiles up)
+    if (total > 0) {
+        build_table(p, R, head, table, (st * 4 + sub) * 32 + lane);
+        if (!meet(sh.heads, meetings, lane)) return false;
+    }
     next.head = head;
     // the first round only fetches; one round past the end meets the heads that are left
 #pragma unroll 1
@@ -990,11 +998,11 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         const int64_t from = (int64_t)blockIdx.x * w.len;
         if (from < w.total) {
             c.left = (int)min((int64_t)w.len, w.total - from);
-            c.head = (int)(from / w.per_head);
+            c.head = quotient(from, w.per_head);
             int64_t rem = from - c.head * w.per_head;
             const int64_t pre = (int64_t)a.row_tiles * a.prefix_tiles;
             if (rem < pre) {
-                c.seg = (int)(rem / a.prefix_tiles);
+                c.seg = quotient(rem, a.prefix_tiles);
                 c.n_tiles = a.prefix_tiles;
                 c.tile = (int)(rem - (int64_t)c.seg * a.prefix_tiles);
             } else {
@@ -1021,7 +1029,7 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         }
         if (lane == 0) {
             sh.total = c.left;
-            sh.last_head = c.left > 0 ? (int)((from + c.left - 1) / w.per_head) : 0;
+            sh.last_head = c.left > 0 ? quotient(from + c.left - 1, w.per_head) : 0;
         }
         if (lane == 0) sh.start = c;
     }
