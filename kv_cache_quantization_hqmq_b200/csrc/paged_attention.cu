@@ -852,6 +852,32 @@ template <int MT, int NT> struct Softmax {
     }
 };
 
+// This thread's row of the piece at c: 16-byte loads of its query, all of a half at once.
+template <int MT, int NT>
+__device__ __forceinline__ void load_query(const PagedAttnArgs &a, Shared<MT> &sh, Softmax<MT, NT> &sm, const Cursor &c,
+                                           const Rows<MT> &rows, int r) {
+    const int gr = rows.base + r;
+    const size_t qr = c.prefix(a) ? ((size_t)(gr / a.G) * a.Hk + c.head) * a.G + gr % a.G
+                                  : ((size_t)(c.seg - a.row_tiles) * a.Hk + c.head) * a.G + r;
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qr * PA_D);
+    constexpr int N = MT == 1 ? 8 : 4;        // 16 bytes at once
+#pragma unroll 1
+    for (int i = 0; i < 16; i += N) {
+        uint4 v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = r < rows.n ? __ldg(src + i + k) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t f = a.q_flip;
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const uint32_t w[8] = {v[k].x ^ f, v[k].y ^ f, v[k].z ^ f, v[k].w ^ f,
+                                   v[k + 1].x ^ f, v[k + 1].y ^ f, v[k + 1].z ^ f, v[k + 1].w ^ f};
+            tmem_st8(sm.lanes + Tmem<MT, NT>::q(sm.g) + 4 * (i + k), w);
+        }
+    }
+    tmem_wait_st();
+    sm.arrive(&sh.q_full[sm.g]);
+}
+
 template <int MT, int NT>
 __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, int warp, int lane) {
     using TM = Tmem<MT, NT>;
@@ -862,6 +888,7 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     Cursor c = sh.start;
     int no = 0, pairs = 0;                    // tiles, and pieces of two groups, so far
     bool cleared = false;                     // P is zero outside this quarter's columns
+    bool loaded = false;                      // the piece's queries are there
     while (c.left > 0) {
         const int n = c.piece();
         const Rows<MT> rows(a, c);
@@ -873,26 +900,9 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
         const int r = rows.rep ? lane : g * 128 + quad * 32 + lane;
         const bool live = r < rows.n;
         const bool pre = at.prefix(a);
-        // the rows' queries
-        {
+        if (!loaded) {
             // (replicated rows keep P where the second group had O)
             if (MT == 2 && rows.rep && pairs > 0 && !mbar_wait(&sh.pair_done, (pairs - 1) & 1)) return false;
-            const int gr = rows.base + r;
-            const size_t qr = pre ? ((size_t)(gr / a.G) * a.Hk + at.head) * a.G + gr % a.G
-                                  : ((size_t)(at.seg - a.row_tiles) * a.Hk + at.head) * a.G + r;
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qr * PA_D);
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-                uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (live) {
-                    v[0] = __ldg(src + 2 * i);
-                    v[1] = __ldg(src + 2 * i + 1);
-                }
-                const uint32_t f = a.q_flip;
-                const uint32_t w[8] = {v[0].x ^ f, v[0].y ^ f, v[0].z ^ f, v[0].w ^ f,
-                                       v[1].x ^ f, v[1].y ^ f, v[1].z ^ f, v[1].w ^ f};
-                tmem_st8(sm.lanes + TM::q(g) + 8 * i, w);
-            }
             if (rows.rep && !cleared) {
                 const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll 1
@@ -902,8 +912,7 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
                 }
             }
             cleared = rows.rep;
-            tmem_wait_st();
-            sm.arrive(&sh.q_full[g]);
+            load_query<MT, NT>(a, sh, sm, at, rows, r);
         }
         sm.ref = sm.m = -INFINITY;
         sm.l = make_float2(0.f, 0.f);
@@ -918,6 +927,16 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             for (int i = 0; i < 2 * n; ++i)
                 if (!sm.half_tile(i == 0, i & 1, reinterpret_cast<const uint32_t *>(sh.mask)[(2 * t0 + i) % (2 * MASK_RING)]))
                     return false;
+        }
+        // the next piece's queries, so that its first scores are under way while this one's output is read
+        // (Q is free: its last scores have come; a change of the rows' kind moves other columns, and waits)
+        loaded = false;
+        if (c.left > 0) {
+            const Rows<MT> to(a, c);
+            if (to.rep == rows.rep && g < to.groups()) {
+                load_query<MT, NT>(a, sh, sm, c, to, to.rep ? lane : g * 128 + quad * 32 + lane);
+                loaded = true;
+            }
         }
         // the piece's partial
         const int lb = MT == 1 || rows.rep ? (no - 1) & 1 : 1;
