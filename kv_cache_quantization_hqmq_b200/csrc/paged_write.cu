@@ -10,8 +10,14 @@
 // The index is the argmax of the exact scores <x, q_p q_s>: fp32 scores decide
 // unless the two best lie within rounding of each other; then fp64 does.
 //   * k_paged_write_table (prefill): the search table of the head names up to 8
-//     candidates per chunk; their codewords sit in shared memory.  A warp keeps
-//     eight tokens and four tokens' table records in flight.
+//     candidates per chunk; their codewords sit in shared memory.  A warp
+//     counts the outliers of its eight tokens, then searches them one by one, the
+//     next one's record under way.  L1 has to hold records and tokens, and
+//     warps to hide their latency: one copy of the codewords (its bank
+//     conflicts cost less than the space; 4 copies, 3 CTAs an SM: 59 us for 4096
+//     tokens, 8 heads, K and V, S = 32) and 64 registers (eight tokens in
+//     registers, two records in flight, 80 registers: 61 us) take 52.5 us,
+//     40 G chunks/s.
 //   * k_paged_write_loop (decode steps, small codebooks, heads without
 //     tables): the loop over the S secondary codewords, y = x conj(q_s)
 //     scoring the 24 primaries at once.  A run of one or two tokens shares each
@@ -24,8 +30,6 @@ namespace hqmq {
 
 constexpr int PW_LOOP_WARPS = 4, PW_TABLE_WARPS = 8;
 constexpr int PW_TOKENS = 8;                  // tokens a warp of the table kernel holds
-constexpr int PW_COPIES = 4;                  // of the codeword table
-constexpr int PW_BATCH = 2;                   // of them, tokens whose records are in flight
 constexpr int PW_SEARCH_FROM = 8;             // tokens of a sequence, on average
 constexpr uint32_t PW_SEARCH_S = 12;
 constexpr int PW_RUNS_FROM = 4;               // tokens of a sequence, on average
@@ -246,7 +250,7 @@ __device__ __forceinline__ uint32_t pick_candidate(const Token &t, uint4 rec, ui
     for (int k = 0; k < LUT_SLOTS; ++k) {
         if ((uint32_t)k >= kmax) break;       // (warp-uniform)
         const uint32_t id = (sl[k >> 1] >> ((k & 1) * 16)) & LUT_ID_MASK;
-        const float4 c = tab[id * PW_COPIES];
+        const float4 c = tab[id];
         const float sc = fmaf(t.x3, c.w, fmaf(t.x2, c.z, fmaf(t.x1, c.y, t.x0 * c.x)));
         const int key = (int)((__float_as_uint(sc) & ~7u) | (7u - k));
         second = max(second, min(key, best));
@@ -351,9 +355,9 @@ __device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t 
 }
 
 template <int DT, int BB>
-__global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 4) k_paged_write_table(const __grid_constant__ WriteArgs a) {
     constexpr int WARPS = PW_TABLE_WARPS, THREADS = WARPS * 32, BLOCK = WARPS * PW_TOKENS;
-    extern __shared__ float4 s_tab[];         // [24 S + 1][PW_COPIES] codewords
+    extern __shared__ float4 s_tab[];         // 24 S + 1 codewords
     __shared__ Run s_run;
     __shared__ float4 s_cb[PG_MAX_S];
     __shared__ uint32_t s_cnt[WARPS + 1];     // outliers of each warp's tokens, and before the block
@@ -365,15 +369,11 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(co
     const float th2 = p.flags ? square_threshold(p.thr[head]) : INFINITY;
     const uint32_t words = 24u * p.S;
     for (uint32_t i = threadIdx.x; i < p.S; i += THREADS) s_cb[i] = __ldg(p.cb + (size_t)head * p.S + i);
-    for (uint32_t e = threadIdx.x; e <= words; e += THREADS) {
-        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e < words) c = codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u));
-#pragma unroll
-        for (int r = 0; r < PW_COPIES; ++r) s_tab[e * PW_COPIES + ((r + e) & (PW_COPIES - 1))] = c;
-    }
+    for (uint32_t e = threadIdx.x; e <= words; e += THREADS)
+        s_tab[e] = e < words ? codeword((int)(e % 24u), __ldg(p.cb + (size_t)head * p.S + e / 24u))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t xt = a.st[role] * (int64_t)(DT == HQMQ_BF16 ? 2 : 4);
     const uint4 *tb = p.table + (size_t)head * LUT_ENTRIES;
-    const float4 *tab = s_tab + (lane & (PW_COPIES - 1));
     const PackConst pc = pack_const(p.b, lane);
     Tally n = {0, 0, 0, 0};
 
@@ -390,21 +390,20 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(co
         // blocks of 64 tokens, 8 to a warp
         for (int b0 = 0; there && b0 < r.n; b0 += BLOCK) {
             const int t0 = b0 + warp * PW_TOKENS, mine = min(max(r.n - t0, 0), PW_TOKENS);
-            RawChunk<DT> x[PW_TOKENS];
-#pragma unroll
-            for (int i = 0; i < PW_TOKENS; ++i) {
-                x[i].zero();
-                if (i < mine) x[i].load(pl.x + (t0 + i) * xt, lane);
-            }
-            uint32_t mask[PW_TOKENS] = {};
+            const char *xw = pl.x + t0 * xt;
             int slot = 0;
             if (p.flags) {
                 int cnt = 0;
+                RawChunk<DT> x[PW_TOKENS];
 #pragma unroll
                 for (int i = 0; i < PW_TOKENS; ++i) {
-                    mask[i] = __ballot_sync(FULL, square_norm(x[i].e(0), x[i].e(1), x[i].e(2), x[i].e(3)) > th2);
-                    if (i >= mine) mask[i] = 0u;              // (a threshold below 0 is passed by zeros)
-                    cnt += __popc(mask[i]);
+                    x[i].zero();
+                    if (i < mine) x[i].load(xw + i * xt, lane);
+                }
+#pragma unroll
+                for (int i = 0; i < PW_TOKENS; ++i) {         // (a threshold below 0 is passed by zeros)
+                    const bool out = square_norm(x[i].e(0), x[i].e(1), x[i].e(2), x[i].e(3)) > th2;
+                    cnt += __popc(__ballot_sync(FULL, i < mine && out));
                 }
                 if (lane == 0) s_cnt[warp] = cnt;
                 if (warp == 0) {              // (a later block: the rows before are this call's, counted in slots)
@@ -420,29 +419,33 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 3) k_paged_write_table(co
                 if (threadIdx.x == 0) s_cnt[WARPS] = all;
             }
             uint32_t unclear = 0;             // tokens of the warp
-#pragma unroll
-            for (int g = 0; g < PW_TOKENS; g += PW_BATCH) {
-                Token k[PW_BATCH];
-                uint4 rec[PW_BATCH];
-#pragma unroll
-                for (int i = 0; i < PW_BATCH; ++i) {
-                    rec[i] = make_uint4(1u << 12, 0u, 0u, 0u);
-                    if (g + i >= mine) continue;              // (warp-uniform)
-                    const RawChunk<DT> &c = x[g + i];
-                    k[i] = {c.e(0), c.e(1), c.e(2), c.e(3), false};
-                    store_token(k[i], p, pl.at0 + t0 + g + i, pl.slots, mask[g + i], slot, lane, n);
-                    slot += __popc(mask[g + i]);
-                    if (k[i].search) rec[i] = __ldg(tb + record_of(k[i].x0, k[i].x1, k[i].x2, k[i].x3));
+            // a token's record is under way while the one before is searched
+            RawChunk<DT> next;
+            next.zero();
+            if (mine > 0) next.load(xw, lane);
+            Token k = {0.f, 0.f, 0.f, 0.f, false};
+            uint4 rec = make_uint4(1u << 12, 0u, 0u, 0u);
+            size_t at = pl.at0 + t0;
+#pragma unroll 1
+            for (int i = 0; i <= mine; ++i, ++at) {
+                const Token ks = k;
+                const uint4 rs = rec;
+                if (i < mine) {
+                    k = {next.e(0), next.e(1), next.e(2), next.e(3), false};
+                    if (i + 1 < mine) next.load(xw + (i + 1) * xt, lane);
+                    uint32_t mask = 0;
+                    if (p.flags) mask = __ballot_sync(FULL, square_norm(k.x0, k.x1, k.x2, k.x3) > th2);
+                    store_token(k, p, at, pl.slots, mask, slot, lane, n);
+                    slot += __popc(mask);
+                    rec = make_uint4(1u << 12, 0u, 0u, 0u);
+                    if (k.search) rec = __ldg(tb + record_of(k.x0, k.x1, k.x2, k.x3));
                 }
-#pragma unroll
-                for (int i = 0; i < PW_BATCH; ++i) {
-                    if (g + i >= mine) continue;
-                    const uint32_t cnt = (rec[i].x >> 12) & 0xFu;
-                    const uint32_t kmax = __reduce_max_sync(FULL, cnt);
+                if (i > 0) {
+                    const uint32_t kmax = __reduce_max_sync(FULL, (rs.x >> 12) & 0xFu);
                     bool clear;
-                    const uint32_t idx = pick_candidate(k[i], rec[i], kmax, tab, clear);
-                    if (!__all_sync(FULL, clear)) unclear |= 1u << (g + i);
-                    pack_group32<BB>(idx, p.b, lane, pc, p.words + (pl.at0 + t0 + g + i) * p.b);
+                    const uint32_t idx = pick_candidate(ks, rs, kmax, s_tab, clear);
+                    if (!__all_sync(FULL, clear)) unclear |= 1u << (i - 1);
+                    pack_group32<BB>(idx, p.b, lane, pc, p.words + (at - 1) * p.b);
                 }
             }
             __syncwarp();
@@ -577,9 +580,9 @@ extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pag
     const uint32_t S = v && v->S > k->S ? v->S : k->S;
     // the tables pay for runs of some tokens (their codewords have to be brought to shared memory) and
     // codebooks of some size (the loop costs about 25 instructions a secondary, the table 250 in all:
-    // 7 sequences of up to 301 tokens, S = 8: 11.5 us by the loop, 35 by the tables; 4096 tokens, S = 32: 131 and 61)
+    // 7 sequences of up to 301 tokens, S = 8: 11.5 us by the loop, 35 by the tables; 4096 tokens, S = 32: 131 and 52)
     const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs && S >= PW_SEARCH_S;
-    const size_t smem = search ? (size_t)(24 * S + 1) * PW_COPIES * sizeof(float4) : 0;
+    const size_t smem = search ? (size_t)(24 * S + 1) * sizeof(float4) : 0;
     // with tables a CTA goes through runs of 64 tokens or more
     const int64_t gx = search && k->page_size < 64 ? (runs * k->page_size + 63) / 64 : runs;
     const dim3 grid((unsigned)gx, (unsigned)k->heads, (unsigned)roles);
