@@ -205,9 +205,6 @@ extern "C" int hqmq_launch_paged_read(const hqmq_kv_pages *c, uint32_t b, int n_
     const size_t smem = (size_t)(24 * c->S + 1) * PR_COPIES * sizeof(float4);
     auto kern = out_dtype == HQMQ_BF16 ? (b == 8 ? k_paged_read<2, 8> : b == 10 ? k_paged_read<2, 10> : k_paged_read<2, 0>)
                                        : (b == 8 ? k_paged_read<1, 8> : b == 10 ? k_paged_read<1, 10> : k_paged_read<1, 0>);
-    if (smem > 32 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return HQMQ_ERR_CUDA;
     const dim3 grid((unsigned)((T + a.span - 1) / a.span), (unsigned)c->heads, (unsigned)n_seqs);
     return launch_pdl(kern, grid, dim3(PR_THREADS), smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }

@@ -29,16 +29,16 @@
 namespace hqmq {
 
 constexpr int PW_LOOP_WARPS = 4, PW_TABLE_WARPS = 8;
-constexpr int PW_TOKENS = 8;                  // tokens a warp of the table kernel holds
+constexpr int PW_TOKENS = 8;                  // tokens of a warp of the table kernel, at most
 constexpr int PW_SEARCH_FROM = 8;             // tokens of a sequence, on average
-constexpr uint32_t PW_SEARCH_S = 12;
+constexpr uint32_t PW_SEARCH_S = 8;
 constexpr int PW_RUNS_FROM = 4;               // tokens of a sequence, on average
 
 struct WriteArgs {
     PagesDev p[2];
     const void *x[2];
     int64_t st[2], sh[2];
-    int n_tokens, n_seqs, max_pages, runs;    // runs: more there cannot be
+    int n_tokens, n_seqs, max_pages;
     const int *cu, *pos0, *table;
     DevStatus *st_out;
 };
@@ -356,7 +356,7 @@ __device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t 
 
 template <int DT, int BB>
 __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 4) k_paged_write_table(const __grid_constant__ WriteArgs a) {
-    constexpr int WARPS = PW_TABLE_WARPS, THREADS = WARPS * 32, BLOCK = WARPS * PW_TOKENS;
+    constexpr int WARPS = PW_TABLE_WARPS, THREADS = WARPS * 32;
     extern __shared__ float4 s_tab[];         // 24 S + 1 codewords
     __shared__ Run s_run;
     __shared__ float4 s_cb[PG_MAX_S];
@@ -377,84 +377,82 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 4) k_paged_write_table(co
     const PackConst pc = pack_const(p.b, lane);
     Tally n = {0, 0, 0, 0};
 
-    for (int item = blockIdx.x; item < a.runs; item += gridDim.x) {
-        if (warp == 0) {
-            const Run r = find_run(a, item, lane);
-            if (lane == 0) s_run = r;
-        }
-        __syncthreads();
-        const Run r = s_run;
-        if (r.n == 0) break;                  // (there are no more)
-        Place pl;
-        const bool there = find_place<DT>(a, p, r, head, role, pl);
-        // blocks of 64 tokens, 8 to a warp
-        for (int b0 = 0; there && b0 < r.n; b0 += BLOCK) {
-            const int t0 = b0 + warp * PW_TOKENS, mine = min(max(r.n - t0, 0), PW_TOKENS);
-            const char *xw = pl.x + t0 * xt;
-            int slot = 0;
-            if (p.flags) {
-                int cnt = 0;
-                RawChunk<DT> x[PW_TOKENS];
+    if (warp == 0) {
+        const Run r = find_run(a, blockIdx.x, lane);
+        if (lane == 0) s_run = r;
+    }
+    __syncthreads();
+    const Run r = s_run;
+    if (r.n == 0) return;
+    Place pl;
+    if (!find_place<DT>(a, p, r, head, role, pl)) return;
+    // blocks of 64 tokens, 8 to a warp; shorter runs in equal shares
+    const int per = min((r.n + WARPS - 1) / WARPS, PW_TOKENS);
+    for (int b0 = 0; b0 < r.n; b0 += WARPS * per) {
+        const int t0 = b0 + warp * per, mine = min(max(r.n - t0, 0), per);
+        const char *xw = pl.x + t0 * xt;
+        int slot = 0;
+        if (p.flags) {
+            int cnt = 0;
+            RawChunk<DT> x[PW_TOKENS];
 #pragma unroll
-                for (int i = 0; i < PW_TOKENS; ++i) {
-                    x[i].zero();
-                    if (i < mine) x[i].load(xw + i * xt, lane);
-                }
-#pragma unroll
-                for (int i = 0; i < PW_TOKENS; ++i) {         // (a threshold below 0 is passed by zeros)
-                    const bool out = square_norm(x[i].e(0), x[i].e(1), x[i].e(2), x[i].e(3)) > th2;
-                    cnt += __popc(__ballot_sync(FULL, i < mine && out));
-                }
-                if (lane == 0) s_cnt[warp] = cnt;
-                if (warp == 0) {              // (a later block: the rows before are this call's, counted in slots)
-                    const uint32_t f = b0 == 0 ? flags_before(p.flags + pl.at0 - r.row0, r.row0, lane) : s_cnt[WARPS];
-                    if (lane == 0) s_cnt[WARPS] = f;
-                }
-                __syncthreads();
-                slot = (int)s_cnt[WARPS];
-                for (int w = 0; w < warp; ++w) slot += (int)s_cnt[w];
-                uint32_t all = s_cnt[WARPS];
-                for (int w = 0; w < WARPS; ++w) all += s_cnt[w];
-                __syncthreads();
-                if (threadIdx.x == 0) s_cnt[WARPS] = all;
+            for (int i = 0; i < PW_TOKENS; ++i) {
+                x[i].zero();
+                if (i < mine) x[i].load(xw + i * xt, lane);
             }
-            uint32_t unclear = 0;             // tokens of the warp
-            // a token's record is under way while the one before is searched
-            RawChunk<DT> next;
-            next.zero();
-            if (mine > 0) next.load(xw, lane);
-            Token k = {0.f, 0.f, 0.f, 0.f, false};
-            uint4 rec = make_uint4(1u << 12, 0u, 0u, 0u);
-            size_t at = pl.at0 + t0;
+#pragma unroll
+            for (int i = 0; i < PW_TOKENS; ++i) {         // (a threshold below 0 is passed by zeros)
+                const bool out = square_norm(x[i].e(0), x[i].e(1), x[i].e(2), x[i].e(3)) > th2;
+                cnt += __popc(__ballot_sync(FULL, i < mine && out));
+            }
+            if (lane == 0) s_cnt[warp] = cnt;
+            if (warp == 0) {              // (a later block: the rows before are this call's, counted in slots)
+                const uint32_t f = b0 == 0 ? flags_before(p.flags + pl.at0 - r.row0, r.row0, lane) : s_cnt[WARPS];
+                if (lane == 0) s_cnt[WARPS] = f;
+            }
+            __syncthreads();
+            slot = (int)s_cnt[WARPS];
+            for (int w = 0; w < warp; ++w) slot += (int)s_cnt[w];
+            uint32_t all = s_cnt[WARPS];
+            for (int w = 0; w < WARPS; ++w) all += s_cnt[w];
+            __syncthreads();
+            if (threadIdx.x == 0) s_cnt[WARPS] = all;
+        }
+        uint32_t unclear = 0;             // tokens of the warp
+        // a token's record is under way while the one before is searched
+        RawChunk<DT> next;
+        next.zero();
+        if (mine > 0) next.load(xw, lane);
+        Token k = {0.f, 0.f, 0.f, 0.f, false};
+        uint4 rec = make_uint4(1u << 12, 0u, 0u, 0u);
+        size_t at = pl.at0 + t0;
 #pragma unroll 1
-            for (int i = 0; i <= mine; ++i, ++at) {
-                const Token ks = k;
-                const uint4 rs = rec;
-                if (i < mine) {
-                    k = {next.e(0), next.e(1), next.e(2), next.e(3), false};
-                    if (i + 1 < mine) next.load(xw + (i + 1) * xt, lane);
-                    uint32_t mask = 0;
-                    if (p.flags) mask = __ballot_sync(FULL, square_norm(k.x0, k.x1, k.x2, k.x3) > th2);
-                    store_token(k, p, at, pl.slots, mask, slot, lane, n);
-                    slot += __popc(mask);
-                    rec = make_uint4(1u << 12, 0u, 0u, 0u);
-                    if (k.search) rec = __ldg(tb + record_of(k.x0, k.x1, k.x2, k.x3));
-                }
-                if (i > 0) {
-                    const uint32_t kmax = __reduce_max_sync(FULL, (rs.x >> 12) & 0xFu);
-                    bool clear;
-                    const uint32_t idx = pick_candidate(ks, rs, kmax, s_tab, clear);
-                    if (!__all_sync(FULL, clear)) unclear |= 1u << (i - 1);
-                    pack_group32<BB>(idx, p.b, lane, pc, p.words + (at - 1) * p.b);
-                }
+        for (int i = 0; i <= mine; ++i, ++at) {
+            const Token ks = k;
+            const uint4 rs = rec;
+            if (i < mine) {
+                k = {next.e(0), next.e(1), next.e(2), next.e(3), false};
+                if (i + 1 < mine) next.load(xw + (i + 1) * xt, lane);
+                uint32_t mask = 0;
+                if (p.flags) mask = __ballot_sync(FULL, square_norm(k.x0, k.x1, k.x2, k.x3) > th2);
+                store_token(k, p, at, pl.slots, mask, slot, lane, n);
+                slot += __popc(mask);
+                rec = make_uint4(1u << 12, 0u, 0u, 0u);
+                if (k.search) rec = __ldg(tb + record_of(k.x0, k.x1, k.x2, k.x3));
             }
-            __syncwarp();
-            for (; unclear; unclear &= unclear - 1u) {
-                const int i = __ffs(unclear) - 1;
-                settle_token<DT, BB>(p, pl.x + (t0 + i) * xt, pl.at0 + t0 + i, s_cb, lane);
+            if (i > 0) {
+                const uint32_t kmax = __reduce_max_sync(FULL, (rs.x >> 12) & 0xFu);
+                bool clear;
+                const uint32_t idx = pick_candidate(ks, rs, kmax, s_tab, clear);
+                if (!__all_sync(FULL, clear)) unclear |= 1u << (i - 1);
+                pack_group32<BB>(idx, p.b, lane, pc, p.words + (at - 1) * p.b);
             }
         }
-        __syncthreads();                      // (s_run, s_cnt)
+        __syncwarp();
+        for (; unclear; unclear &= unclear - 1u) {
+            const int i = __ffs(unclear) - 1;
+            settle_token<DT, BB>(p, pl.x + (t0 + i) * xt, pl.at0 + t0 + i, s_cb, lane);
+        }
     }
     n.add_to(a.st_out, lane);
 }
@@ -575,24 +573,19 @@ extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pag
     // a sequence's n tokens touch at most (n - 1) / P + 2 pages, and no more than n
     int64_t runs = (int64_t)n_tokens / k->page_size + 2ll * n_seqs;
     if (runs > n_tokens) runs = n_tokens;
-    a.runs = (int)runs;
     const int roles = v ? 2 : 1;
     const uint32_t S = v && v->S > k->S ? v->S : k->S;
     // the tables pay for runs of some tokens (their codewords have to be brought to shared memory) and
-    // codebooks of some size (the loop costs about 25 instructions a secondary, the table 250 in all:
-    // 7 sequences of up to 301 tokens, S = 8: 11.5 us by the loop, 35 by the tables; 4096 tokens, S = 32: 131 and 52)
+    // codebooks of some size (the loop costs about 25 instructions a secondary).  8 heads, K and V, loop and
+    // table: 4096 tokens, pages of 64: S = 32 131 and 51 us, S = 8 69 and 41; 32 sequences of 24 tokens at
+    // S = 8: 15.5 and 15.2 us in pages of 64, 13.9 and 15.2 in pages of 16
     const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs && S >= PW_SEARCH_S;
     const size_t smem = search ? (size_t)(24 * S + 1) * sizeof(float4) : 0;
-    // with tables a CTA goes through runs of 64 tokens or more
-    const int64_t gx = search && k->page_size < 64 ? (runs * k->page_size + 63) / 64 : runs;
-    const dim3 grid((unsigned)gx, (unsigned)k->heads, (unsigned)roles);
+    const dim3 grid((unsigned)runs, (unsigned)k->heads, (unsigned)roles);
     const uint32_t bb = v && bv != bk ? 0 : bk;
     const bool runs_of_some = n_tokens >= PW_RUNS_FROM * n_seqs;
     auto kern = dtype == HQMQ_BF16 ? write_kernel<HQMQ_BF16>(bb, search, runs_of_some)
                                    : write_kernel<HQMQ_F32>(bb, search, runs_of_some);
-    if (smem > 32 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return HQMQ_ERR_CUDA;
     const dim3 block((search ? PW_TABLE_WARPS : PW_LOOP_WARPS) * 32);
     return launch_pdl(kern, grid, block, smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }
