@@ -1,6 +1,5 @@
-// paged.cuh -- the paged coded cache on the device: its record, the lookups
-// of a token's codes and the host-side conversion (include/hqmq.h,
-// hqmq_kv_pages).
+// paged.cuh -- the paged coded cache on the device: its record and the
+// host-side conversion (include/hqmq.h, hqmq_kv_pages).
 #pragma once
 
 #include "hqmq_device.cuh"
@@ -48,13 +47,6 @@ inline PagesDev pages_dev(const hqmq_kv_pages *p, uint32_t b) {
     d.heads = p->heads;
     d.cap = p->flags ? p->out_cap : 0;
     return d;
-}
-
-// Index of chunk c in a token's b words.
-__device__ __forceinline__ uint32_t token_index(const uint32_t *w, uint32_t b, int c) {
-    const uint32_t p = (uint32_t)c * b, i = p >> 5;
-    const uint32_t lo = __ldg(w + i), hi = __ldg(w + (i + 1 < b ? i + 1 : i));
-    return __funnelshift_r(lo, hi, p & 31u) & ((1u << b) - 1u);
 }
 
 // Flagged chunks in rows [0, row) of a (page, head): one warp, all lanes get

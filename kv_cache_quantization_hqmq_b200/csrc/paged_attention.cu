@@ -25,13 +25,27 @@
 //   * two threads issue the products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
-//     softmax in base 2, P back as two bf16 terms P_hi + P_lo (about 16
-//     significant bits).  The reference maximum moves only when a row's
+//     softmax in base 2, P back as bf16: one term for bf16 outputs (its
+//     2^-9 is the output's own rounding), three for fp32 outputs (2^-24, so
+//     that fp32 outputs are fp32 accurate; two would leave 2^-17).  The sum is
+//     taken in fp32 before the rounding.  The reference maximum moves only when a row's
 //     maximum has grown by more than 2^8 (then O is rescaled in tensor
 //     memory): weights up to 2^8 lose nothing in floating point.
 // Segments with at most 32 rows put the same rows into each of the four
 // 32-lane quarters; quarter w takes columns 16 w .. 16 w + 15 of every tile
 // (the others get weight 0) and keeps a partial of its own.
+//
+// MT = 2 (bf16 outputs, more than 128 rows over the prefix) decodes a tile once
+// for 256 rows instead of twice: what bounds it is not the products (1024
+// clocks a tile at 16384 multiply-adds a clock) but the chain scores -> softmax
+// -> P V -> next scores of its two half-tile buffers, beside which the
+// producers' decoding fits.  Measured (bf16, S = 32, 8 KV heads, pages of 64):
+// 32 sequences of 1000 tokens behind 131072: 213 us, 138 GFLOP at 650 TFLOP/s,
+// 272 MB of codes (an earlier step, at 228: with the decoding left out 189 us, with decoding, softmax
+// arithmetic and products left out 133 us, the hand-overs' latency).  A score
+// step of 64 tokens without double buffers took 235 us, one thread for all
+// products 259 us.  One group of 128 rows (MT = 1) spends its time on the
+// pieces' ends and the decoding: 16 sequences of 500 tokens behind 8191: 32 us.
 //
 // Every wait is bounded; one that runs out sets HQMQ_FLAG_TIMEOUT.
 #include "paged.cuh"
@@ -43,7 +57,9 @@ constexpr int PA_D = 128;
 constexpr int PA_TILE = 64;                   // tokens of a tile
 constexpr int PA_PART = 132;                  // floats of a row's partial: m, l, -, -, O[128]
 constexpr int PA_CTAS = 148;                  // one per SM of a B200
-constexpr int PA_REP_ROWS = 32;               // segments up to this many rows are replicated
+// Segments up to this many rows are replicated (prefix of 4096, 8 rows a head, 32 heads, own parts of up to
+// 1111 tokens: 52 us; 54 with the prefix's rows in one quarter only).
+constexpr int PA_REP_ROWS = 32;
 constexpr float PA_RESCALE = 8.0f;
 constexpr int TILE_BYTES = PA_TILE * PA_D * 2;
 constexpr int META_RING = 4;                  // tiles
@@ -562,7 +578,7 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
 }
 
 // ---------------------------------------------------------------------------
-// the matrix products: one thread
+// the matrix products: a thread for the scores, one for P V
 // ---------------------------------------------------------------------------
 // Steps are tiles (buffer = stage) or, for two groups, half tiles (buffer =
 // half).  Each step of a group goes scores -> softmax -> P V; where P replaces
@@ -1192,7 +1208,8 @@ struct PartPlan {
 inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len, int out_dtype) {
     PartPlan p;
     const int64_t rows = (int64_t)B * (Hq / Hk);
-    // fp32 outputs take three terms of P, which leaves tensor memory for one group of rows
+    // fp32 outputs take three terms of P, which leaves tensor memory for one group of rows.  (256 rows over
+    // 131072 tokens, bf16: 215 us as two groups at once, 304 as one after the other.)
     p.mt = prefix_len > 0 && rows > 128 && out_dtype == HQMQ_BF16 ? 2 : 1;
     p.row_tiles = prefix_len > 0 ? (int)((rows + 128 * p.mt - 1) / (128 * p.mt)) : 0;
     p.prefix_slot_rows = rows <= PA_REP_ROWS ? (int)(4 * rows) : 128 * p.mt;
@@ -1219,7 +1236,7 @@ static int launch_paged_attn_b(const PagedAttnArgs &a, int ctas, void *o, int ou
 
 template <int MT, int NT>
 static int launch_paged_attn(PagedAttnArgs &a, int ctas, void *o, int out_dtype, float *lse, cudaStream_t stream) {
-    // 8 table copies (no bank conflicts) where they fit, K's first
+    // 8 table copies (no bank conflicts) where they fit, K's first (S = 8, 32 heads: 52 us; 57 with 4 of each)
     const auto fits = [&](uint32_t rk, uint32_t rv) {
         return attn_table_end(a.k.S, rk, a.v.S, rv) + sizeof(Shared<MT>) <= 227 * 1024;
     };
