@@ -406,9 +406,14 @@ _BF16, _F32, _I32, _F64 = torch.bfloat16, torch.float32, torch.int32, torch.floa
 _DTYPE_CODE = {torch.bfloat16: HQMQ_BF16, torch.float32: HQMQ_F32}
 
 
+# torch.cuda.current_device without its check that CUDA is up: tensors on a device are there already, and
+# without any the answer does not match theirs
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _here(*tensors):
     """The current CUDA device, on which all of the tensors have to be (the calls launch there)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:       # (-1 for a CPU tensor)
             raise ValueError("tensors must be on the current CUDA device %d, got one on %s "
@@ -515,12 +520,11 @@ _pack_view = struct.Struct("=4qi4x").pack                # its bytes
 assert ctypes.sizeof(_HeadView) == 40 == len(_pack_view(0, 0, 0, 0, 0))
 
 
-def _head_view(x):
+def _head_view(x, heads, D):
     sb, st, sh, sd = x.stride()
-    s = x.shape
-    if sd != 1 and s[3] > 1:
+    if sd != 1 and D > 1:
         raise ValueError("the last dimension must be contiguous")
-    return _pack_view(x.data_ptr(), sb, st, sh, s[2])
+    return _pack_view(x.data_ptr(), sb, st, sh, heads)
 
 
 def rope_inv_freq(R, base=10000.0, device="cuda"):
@@ -537,25 +541,27 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
     x = q if q is not None else k
     if x is None or x.dim() != 4:
         raise ValueError("q and k are [B, T, heads, D]")
-    B, T, _, D = x.shape
-    dt = x.dtype
-    views = []
-    for t, t_out, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
+    shape, dt = x.shape, x.dtype
+    B, T, _, D = shape
+    views, w, w_dt = [], None, HQMQ_BF16
+    for t, t_out, wt in ((q, q_out, q_weight), (k, k_out, k_weight)):
         if t is None:
-            if t_out is not None or w is not None:
+            if t_out is not None or wt is not None:
                 raise ValueError("an output or weight without its input")
             views += (None, None)
             continue
-        s = t.shape
-        if t_out is None or len(s) != 4 or s[0] != B or s[1] != T or s[3] != D or t_out.shape != s or \
-                t.dtype is not dt or t_out.dtype is not dt:
+        s = shape if t is x else t.shape
+        if t_out is None or len(s) != 4 or t_out.shape != s or t.dtype is not dt or t_out.dtype is not dt or \
+                (t is not x and (s[0] != B or s[1] != T or s[3] != D)):
             raise ValueError("q, k and their outputs must agree in B, T, D and dtype")
-        if w is not None and (w.shape != (D,) or not w.is_contiguous()):
-            raise ValueError("weights are contiguous [D]")
-        views += (_head_view(t), _head_view(t_out))
-    w = q_weight if q_weight is not None else k_weight
-    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
-        raise ValueError("the weights must have one dtype")
+        if wt is not None:
+            if wt.dim() != 1 or wt.shape[0] != D or not wt.is_contiguous():
+                raise ValueError("weights are contiguous [D]")
+            if w is not None and wt.dtype is not w.dtype:
+                raise ValueError("the weights must have one dtype")
+            w, w_dt = wt, _code(wt)
+        v = _head_view(t, s[2], D)
+        views += (v, v if t_out is t else _head_view(t_out, s[2], D))
     R = 0
     if inv_freq is not None:
         if inv_freq.dtype is not _F64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -564,8 +570,7 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
         _ints("pos", pos, (B, T))
     dev = _here(q, k, q_out, k_out, pos, inv_freq, q_weight, k_weight)
     rc = _lib.hqmq_qk_norm_rope(
-        *views, _code(x), B, T, D, _addr(q_weight), _addr(k_weight), HQMQ_BF16 if w is None else _code(w),
-        eps, _addr(pos), _addr(inv_freq), R, 1 if interleaved else 0, _on(stream, dev))
+        *views, _code(x), B, T, D, _addr(q_weight), _addr(k_weight), w_dt, eps, _addr(pos), _addr(inv_freq), R, 1 if interleaved else 0, _on(stream, dev))
     if rc:
         _check("hqmq_qk_norm_rope", rc)
 
