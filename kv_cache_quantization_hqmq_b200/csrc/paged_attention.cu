@@ -22,7 +22,7 @@
 //     tiles [64 tokens][128]
 //     in the tensor core's 128-byte swizzle: K is the K-major B operand of
 //     S = Q K^T, V, in the same layout, the MN-major B operand of O += P V;
-//   * two threads issue the products (tcgen05.mma, 128 rows, accumulators
+//   * two warps issue the products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
 //     softmax in base 2, P back as bf16: one term for bf16 outputs (its
@@ -40,12 +40,12 @@
 // clocks a tile at 16384 multiply-adds a clock) but the chain scores -> softmax
 // -> P V -> next scores of its two half-tile buffers, beside which the
 // producers' decoding fits.  Measured (bf16, S = 32, 8 KV heads, pages of 64):
-// 32 sequences of 1000 tokens behind 131072: 213 us, 138 GFLOP at 650 TFLOP/s,
+// 32 sequences of 1000 tokens behind 131072: 204 us, 138 GFLOP at 675 TFLOP/s,
 // 272 MB of codes (an earlier step, at 228: with the decoding left out 189 us, with decoding, softmax
 // arithmetic and products left out 133 us, the hand-overs' latency).  A score
-// step of 64 tokens without double buffers took 235 us, one thread for all
+// step of 64 tokens without double buffers took 235 us, one warp for all
 // products 259 us.  One group of 128 rows (MT = 1) spends its time on the
-// pieces' ends and the decoding: 16 sequences of 500 tokens behind 8191: 32 us.
+// pieces' ends and the decoding: 16 sequences of 500 tokens behind 8191: 31 us.
 //
 // Every wait is bounded; one that runs out sets HQMQ_FLAG_TIMEOUT.
 #include "paged.cuh"
@@ -578,14 +578,17 @@ __device__ __forceinline__ bool produce(const PagedAttnArgs &a, Shared<MT> &sh, 
 }
 
 // ---------------------------------------------------------------------------
-// the matrix products: a thread for the scores, one for P V
+// the matrix products: a warp for the scores, one for P V
 // ---------------------------------------------------------------------------
 // Steps are tiles (buffer = stage) or, for two groups, half tiles (buffer =
 // half).  Each step of a group goes scores -> softmax -> P V; where P replaces
-// S, the next scores in that buffer wait for P V.  A wait or an arrival costs
-// a thread some 100 clocks, so the two products have a thread each, and one
-// copy of code serves every stage, buffer and group (instruction fetch, too,
-// is a limit of a kernel with so many roles).
+// S, the next scores in that buffer wait for P V.  Under the producers' load on
+// shared memory a look at a barrier takes some 250 clocks, so the two products
+// have a warp each (of which one lane issues), the softmax looks ahead, and one
+// copy of code serves every stage, buffer and group (instruction fetch, too, is
+// a limit of a kernel with so many roles).  Weights in columns of their own,
+// so that the next scores need not wait for P V, take one more barrier in the
+// softmax: 224 us for 207 (131072 tokens, 256 rows).
 struct Operands {
     static constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);    // descriptor: sbo, version, swizzle
     uint32_t k_lo, v_lo;
@@ -594,7 +597,7 @@ struct Operands {
 };
 
 template <int MT, int NT>
-__device__ __forceinline__ bool issue_scores(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles) {
+__device__ __forceinline__ bool issue_scores(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles, bool leader) {
     using TM = Tmem<MT, NT>;
     const Operands op(tiles);
     Cursor c = sh.start;
@@ -622,12 +625,14 @@ __device__ __forceinline__ bool issue_scores(const PagedAttnArgs &a, Shared<MT> 
                 tc_fence_after();
                 const uint32_t d = two ? TM::s(b) : TM::half(g, h), q = TM::q(g);
                 const uint32_t lo = op.k_lo + st * (TILE_BYTES >> 4) + h * (32 * 128 / 16);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)   // 32 bytes of a row; the second 64 elements in the next block
-                    mma_ts(d, q + k * 8, lo + (k >> 2) * (TILE_BYTES / 2 / 16) + (k & 3) * 2, op.HI, idesc, k > 0);
-                mma_commit(&sh.s_full[g][b]);
+                    for (int k = 0; k < 8; ++k)   // 32 bytes of a row; the second 64 elements in the next block
+                        mma_ts(d, q + k * 8, lo + (k >> 2) * (TILE_BYTES / 2 / 16) + (k & 3) * 2, op.HI, idesc, k > 0);
+                    mma_commit(&sh.s_full[g][b]);
+                }
             }
-            mma_commit(&sh.k_empty[st]);
+            if (leader) mma_commit(&sh.k_empty[st]);
         }
         c.skip(a, n);
     }
@@ -635,7 +640,7 @@ __device__ __forceinline__ bool issue_scores(const PagedAttnArgs &a, Shared<MT> 
 }
 
 template <int MT, int NT>
-__device__ __forceinline__ bool issue_outputs(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles) {
+__device__ __forceinline__ bool issue_outputs(const PagedAttnArgs &a, Shared<MT> &sh, uint32_t tiles, bool leader) {
     using TM = Tmem<MT, NT>;
     constexpr uint32_t idesc = mma_idesc(128, PA_D, true);
     const Operands op(tiles);
@@ -658,19 +663,22 @@ __device__ __forceinline__ bool issue_outputs(const PagedAttnArgs &a, Shared<MT>
                 if (!mbar_wait(&sh.p_full[g][b], (ph >> (2 * g + b)) & 1)) return false;
                 ph ^= 1u << (2 * g + b);
                 tc_fence_after();
+                const uint32_t acc = (add >> g) & 1u;
+                add |= 1u << g;
                 const uint32_t o = TM::o(g), pc = two ? TM::p(b) : TM::half(g, h);
                 const uint32_t lo = op.v_lo + st * (TILE_BYTES >> 4) + h * (32 * 128 / 16);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < PA_TILE / 16; ++k) {
-                    if (k == 2 && !two) break;
+                    for (int k = 0; k < PA_TILE / 16; ++k) {
+                        if (k == 2 && !two) break;
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
-                        mma_ts(o, pc + p_col<NT>(k, x), lo + k * 128, op.HI, idesc, k || x ? 1u : (add >> g) & 1u);
+                        for (int x = 0; x < NT; ++x)
+                            mma_ts(o, pc + p_col<NT>(k, x), lo + k * 128, op.HI, idesc, k || x ? 1u : acc);
+                    }
+                    mma_commit(&sh.p_empty[g][b]);
                 }
-                add |= 1u << g;
-                mma_commit(&sh.p_empty[g][b]);
             }
-            mma_commit(&sh.v_empty[st]);
+            if (leader) mma_commit(&sh.v_empty[st]);
         }
         c.skip(a, n);
     }
@@ -756,6 +764,7 @@ template <int MT, int NT> struct Softmax {
     float ref, m;                             // exponents are relative to ref; largest score so far (times sl2)
     float2 l;
     uint32_t ph;                              // phases of the group's two buffers
+    uint32_t there;                           // the next step's scores are there
 
     __device__ __forceinline__ void arrive(uint64_t *bar) {
         tc_fence_before();
@@ -798,7 +807,8 @@ template <int MT, int NT> struct Softmax {
 
     // Replicated rows: 16 of the columns of the piece's tile i, in buffer b.
     __device__ __forceinline__ bool tile_rep(int i, int b, const uint2 &valid) {
-        if (!mbar_wait(&sh.s_full[0][b], (ph >> b) & 1)) return false;
+        const uint32_t p_there = mbar_test(&sh.p_empty[0][b], ((ph >> b) & 1) ^ 1);
+        if (!there && !mbar_wait(&sh.s_full[0][b], (ph >> b) & 1)) return false;
         tc_fence_after();
         const uint32_t mask = ((quad & 2 ? valid.y : valid.x) >> (16 * (quad & 1))) & 0xFFFFu;
         uint32_t s[16];
@@ -807,9 +817,10 @@ template <int MT, int NT> struct Softmax {
         arrive(&sh.s_empty[0][b]);
         if (mask != 0xFFFFu) hide(s, mask);
         if (!rescale(row_max<16>(s), i > 0 ? &sh.p_empty[0][b ^ 1] : nullptr, ((ph >> (b ^ 1)) & 1) ^ 1)) return false;
-        if (!mbar_wait(&sh.p_empty[0][b], ((ph >> b) & 1) ^ 1)) return false;
+        if (!p_there && !mbar_wait(&sh.p_empty[0][b], ((ph >> b) & 1) ^ 1)) return false;
         tc_fence_after();
         put(s, ref == -INFINITY ? 0.f : ref, lanes + TM::p(b) + p_col<NT>(quad, 0));
+        there = mbar_test(&sh.s_full[0][b ^ 1], (ph >> (b ^ 1)) & 1);
         tmem_wait_st();
         arrive(&sh.p_full[0][b]);
         ph ^= 1u << b;
@@ -817,7 +828,8 @@ template <int MT, int NT> struct Softmax {
     }
     // A row per thread, one group: all 64 columns of tile i, in buffer b.
     __device__ __forceinline__ bool tile_full(int i, int b, const uint2 &valid) {
-        if (!mbar_wait(&sh.s_full[g][b], (ph >> b) & 1)) return false;
+        const uint32_t p_there = mbar_test(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1);
+        if (!there && !mbar_wait(&sh.s_full[g][b], (ph >> b) & 1)) return false;
         tc_fence_after();
         const uint2 mask = valid;
         uint32_t s0[32], s1[32];
@@ -830,7 +842,7 @@ template <int MT, int NT> struct Softmax {
         if (!rescale(fmaxf(row_max<32>(s0), row_max<32>(s1)), i > 0 ? &sh.p_empty[g][b ^ 1] : nullptr,
                      ((ph >> (b ^ 1)) & 1) ^ 1))
             return false;
-        if (!mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
+        if (!p_there && !mbar_wait(&sh.p_empty[g][b], ((ph >> b) & 1) ^ 1)) return false;
         tc_fence_after();
         const float rf = ref == -INFINITY ? 0.f : ref;
         const uint32_t tp = lanes + TM::p(b);
@@ -838,6 +850,7 @@ template <int MT, int NT> struct Softmax {
         put(s0 + 16, rf, tp + p_col<NT>(1, 0));
         put(s1, rf, tp + p_col<NT>(2, 0));
         put(s1 + 16, rf, tp + p_col<NT>(3, 0));
+        there = mbar_test(&sh.s_full[g][b ^ 1], (ph >> (b ^ 1)) & 1);
         tmem_wait_st();
         arrive(&sh.p_full[g][b]);
         ph ^= 1u << b;
@@ -845,7 +858,7 @@ template <int MT, int NT> struct Softmax {
     }
     // A row per thread, two groups: half h of a tile, its weights in the place of its scores.
     __device__ __forceinline__ bool half_tile(bool first, int h, const uint32_t &valid) {
-        if (!mbar_wait(&sh.s_full[g][h], (ph >> h) & 1)) return false;
+        if (!there && !mbar_wait(&sh.s_full[g][h], (ph >> h) & 1)) return false;
         tc_fence_after();
         const uint32_t mask = valid, ts = lanes + TM::half(g, h);
         uint32_t s[32];
@@ -856,6 +869,7 @@ template <int MT, int NT> struct Softmax {
         const float rf = ref == -INFINITY ? 0.f : ref;
         put(s, rf, ts);
         put(s + 16, rf, ts + 8);
+        there = mbar_test(&sh.s_full[g][h ^ 1], (ph >> (h ^ 1)) & 1);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -899,7 +913,7 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
     using TM = Tmem<MT, NT>;
     const int quad = warp & 3;
     Softmax<MT, NT> sm = {a, sh, warp >> 2, quad, lane, (uint32_t)(quad * 32) << 16, 0.f, 0.f,
-                          make_float2(0.f, 0.f), 0u};
+                          make_float2(0.f, 0.f), 0u, 0u};
     const int g = sm.g;
     Cursor c = sh.start;
     int no = 0, pairs = 0;                    // tiles, and pieces of two groups, so far
@@ -930,6 +944,7 @@ __device__ __forceinline__ bool softmax(const PagedAttnArgs &a, Shared<MT> &sh, 
             cleared = rows.rep;
             load_query<MT, NT>(a, sh, sm, at, rows, r);
         }
+        sm.there = 0;
         sm.ref = sm.m = -INFINITY;
         sm.l = make_float2(0.f, 0.f);
         if (rows.rep) {
@@ -1084,12 +1099,11 @@ __global__ void __launch_bounds__(Roles<MT>::THREADS, 1) k_paged_attn(const __gr
         if (warp < PRODUCTS) {
             ok = scout<MT>(a, sh, warp - SCOUT, lane);
         } else {
-            if (elect_one()) {
-                ok = sh.tmem == 0u && (warp == PRODUCTS ? issue_scores<MT, NT>(a, sh, tiles)
-                                                        : issue_outputs<MT, NT>(a, sh, tiles));
-                mma_commit(&sh.drain[warp - PRODUCTS]);       // nothing may be in flight when tensor memory goes
-                if (!mbar_wait(&sh.drain[warp - PRODUCTS], 0)) ok = false;
-            }
+            const bool leader = elect_one();
+            ok = sh.tmem == 0u && (warp == PRODUCTS ? issue_scores<MT, NT>(a, sh, tiles, leader)
+                                                    : issue_outputs<MT, NT>(a, sh, tiles, leader));
+            if (leader) mma_commit(&sh.drain[warp - PRODUCTS]);   // nothing may be in flight when tensor memory goes
+            if (!mbar_wait(&sh.drain[warp - PRODUCTS], 0)) ok = false;
             __syncwarp();
         }
     }
