@@ -174,3 +174,88 @@ def test_the_contiguous_cache_gives_the_same():
             want, bound, _, _ = plain(q[b, rows].float().cpu().numpy(), k, v, np.ones(T, bool), D ** -0.5)
             assert np.all(np.abs(layer.o[b, rows].double().cpu().numpy() - want) <= 2 * bound)
             assert np.all(np.abs(o[b, rows].double().cpu().numpy() - want) <= 2 * (bound + 2.0 ** -16 * 2 * np.abs(v).max()))
+
+
+@pytest.mark.parametrize("S,cap,out", [((8, 32), (0, 60), torch.float32), ((32, 8), (40, 0), BF), ((48, 3), (64, 9), BF),
+                                       ((10, 22), (30, 30), torch.float32)])
+def test_keys_and_values_of_different_codebooks(S, cap, out):
+    """K and V with codebooks and outlier slots of their own, pools of different sizes; prefixes that end in
+    different rows of a page; queries and outputs in one buffer."""
+    rng = np.random.default_rng(S[0])
+    B, Hk, G, page = 3, 2, 4, 32
+    lens, prefix = [33, 0, 70], 45
+    table, n = layout(rng, [m + 1 for m in lens], page, spare=3)
+    ptable = np.setdiff1d(np.arange(n), table)[:2].astype(np.int32)
+    pools = [P.empty_pool(rng, n + 4 * r, Hk, page, S[r], cap[r]) for r in range(2)]
+    kv = [P.upload(p, P.search_tables(p["cb"])) for p in pools]
+    status = hqmq.new_status()
+    for tab, m in ((ptable[None], [prefix]), (table, lens), (table, [1] * B)):
+        old = lens if m == [1] * B else [0] * len(m)
+        cu = np.concatenate([[0], np.cumsum(m)])
+        x = [torch.randn(int(cu[-1]), Hk, D, generator=torch.Generator().manual_seed(r)).to(BF) for r in range(2)]
+        x[0][:, :, 7] *= 9
+        hqmq.hqmq_paged_write(x[0].cuda(), x[1].cuda(), kv[0][0], kv[1][0], *cuda_ints(tab, cu, old), status=status)
+        for pool, y in zip(pools, x):
+            P.write(pool, y.float().numpy(), tab, cu, old)
+    for pool, (_, t) in zip(pools, kv):
+        P.assert_pools_equal(t, pool)
+    lens = [m + 1 for m in lens]
+    q = torch.randn(B, Hk * G, D, generator=torch.Generator().manual_seed(9)).to(BF)
+    qo = q.cuda()
+    o = qo if out == BF else torch.empty(B, Hk * G, D, device="cuda")      # (bf16: in place)
+    ws = hqmq.alloc_attention_paged_ws(B, Hk * G, kv[0][0], table.shape[1], prefix)
+    t_d, len_d, pt_d = cuda_ints(table, lens, ptable)
+    hqmq.hqmq_attention_paged(qo, kv[0][0], kv[1][0], t_d, len_d, o, ws, prefix_table=pt_d, prefix_len=prefix,
+                              status=status)
+    for b, m in enumerate(lens):
+        k, v = (P.bf16(np.concatenate([P.dense(p, ptable, prefix)[0], P.dense(p, table[b], m)[0]], 1)) for p in pools)
+        for h in range(Hk):
+            rows = slice(h * G, (h + 1) * G)
+            want, bound, _, _ = plain(q[b, rows].float().numpy(), k[h], v[h], np.ones(prefix + m, bool), D ** -0.5, out)
+            tol = 2 * bound + (2.0 ** -8 * np.abs(want) if out == BF else 0)
+            assert np.all(np.abs(o[b, rows].double().cpu().numpy() - want) <= tol)
+    assert hqmq.read_status(status)["flags"] & ~hqmq.FLAG_OUTLIER_OVERFLOW == 0
+
+
+def test_two_streams_and_two_graphs():
+    """Calls on two streams at once with workspaces of their own, and two graphs that share one workspace."""
+    layers = [Layer(s, 32, 32, 64, 2, 4, 70, [40, 9, 64], True, BF) for s in (1, 2)]
+    for layer in layers:
+        layer.fill(layer.ptable, [layer.prefix])
+        layer.fill(layer.table, layer.lens)
+    q = torch.randn(2, 3, 8, D, generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+
+    def attend(layer, x, ws):
+        hqmq.hqmq_attention_paged(x, layer.kp, layer.vp, layer.t_d, layer.len_d, layer.o, ws, prefix_table=layer.pt_d,
+                                  prefix_len=layer.prefix, lse=layer.lse, status=layer.status)
+
+    want = []
+    for i, layer in enumerate(layers):
+        attend(layer, q[i], layer.ws)
+        want.append((layer.o.clone(), layer.lse.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for layer in layers:
+        layer.o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (layer, s) in enumerate(zip(layers, streams)):
+            with torch.cuda.stream(s):
+                attend(layer, q[i], layer.ws)
+    torch.cuda.synchronize()
+    for layer, (o, lse) in zip(layers, want):
+        assert torch.equal(layer.o, o) and torch.equal(layer.lse, lse)
+        layer.o.zero_()
+    graphs = []
+    for i, layer in enumerate(layers):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            attend(layer, q[i], layers[0].ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for layer, (o, lse) in zip(layers, want):
+        assert torch.equal(layer.o, o) and torch.equal(layer.lse, lse)
+        assert hqmq.read_status(layer.status)["flags"] & ~hqmq.FLAG_OUTLIER_OVERFLOW == 0
