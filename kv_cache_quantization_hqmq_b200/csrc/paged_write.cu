@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(PW_LOOP_WARPS * 32, CTAS) k_paged_write_loop(c
     RawChunk<DT> next;
     next.zero();
     if (own < r.n) next.load(pl.x + own * xt, lane);
-    uint32_t before = 0;                      // flagged chunks before the tokens of this round
+    uint32_t before = 0;                      // flagged chunks before the tokens of this turn
     if (p.flags) before = flags_before(p.flags + pl.at0 - r.row0, r.row0, lane);
     if (threadIdx.x < p.S) s_cb[threadIdx.x] = q;
     const float th2 = p.flags ? square_threshold(thr) : INFINITY;

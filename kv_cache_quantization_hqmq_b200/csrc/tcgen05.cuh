@@ -129,12 +129,5 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle: rows of 128 bytes in groups of
-// eight (sbo bytes apart); lbo: bytes between 64-element blocks of an MN-major
-// operand (unused K-major).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
-}
 
 }  // namespace hqmq
