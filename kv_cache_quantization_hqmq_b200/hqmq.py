@@ -443,11 +443,11 @@ def _ints(name, t, shape):
                          % (name, shape, t.dtype, tuple(t.shape)))
 
 
-def _table(t, n_seqs, name="block_table"):
+def _table(t, n_seqs=None, name="block_table"):
     s = t.shape
-    if len(s) != 2 or s[0] != n_seqs or t.dtype is not _I32 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 [%d, max_pages], got %s %s"
-                         % (name, n_seqs, t.dtype, tuple(s)))
+    if len(s) != 2 or (n_seqs is not None and s[0] != n_seqs) or t.dtype is not _I32 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 [n_seqs, max_pages], got %s %s"
+                         % (name, t.dtype, tuple(s)))
     return s[1]
 
 
@@ -575,33 +575,27 @@ def hqmq_qk_norm_rope(q, k, q_out, k_out, pos, inv_freq, q_weight=None, k_weight
         _check("hqmq_qk_norm_rope", rc)
 
 
-def _new_tokens(x, heads):
-    s = x.shape
-    if len(s) != 3 or s[1] != heads or s[2] != 128 or x.stride(2) != 1:
-        raise ValueError("new tokens are [n_tokens, %d, 128] with a contiguous last dimension, got "
-                         "%s" % (heads, tuple(s)))
-
-
 def hqmq_paged_write(xk, xv, k, v, block_table, cu_tokens, pos0, status=None, stream=None):
     """Quantises new tokens xk, xv ([n_tokens, heads, 128], bf16 or fp32, any token
     and head strides) into the pages k, v (KVPages): sequence b's are rows
     cu_tokens[b] .. cu_tokens[b+1]-1 and go to positions pos0[b], pos0[b]+1, ...
     block_table: int32 [n_seqs, max_pages]; cu_tokens: int32 [n_seqs + 1]; pos0:
     int32 [n_seqs].  xv and v may be None."""
-    _new_tokens(xk, k.heads)
-    ks, vs, v_ref, v_keep = xk.stride(), (0, 0), None, None
+    s, ks, vs, v_ref, v_keep = xk.shape, xk.stride(), (0, 0, 1), None, None
     if v is not None:
-        _new_tokens(xv, v.heads)
-        if xv.shape != xk.shape or xv.dtype is not xk.dtype:
+        if xv.shape != s or xv.dtype is not xk.dtype:
             raise ValueError("xk and xv must agree in shape and dtype")
         vs, v_ref, v_keep = xv.stride(), v._ref, v._keep[0]
-    n_seqs = pos0.shape[0] if pos0.dim() == 1 else -1
+    if len(s) != 3 or s[1] != k.heads or s[2] != 128 or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("new tokens are [n_tokens, %d, 128] with a contiguous last dimension, got "
+                         "%s" % (k.heads, tuple(s)))
+    max_pages = _table(block_table)
+    n_seqs = block_table.shape[0]
     _ints("pos0", pos0, (n_seqs,))
     _ints("cu_tokens", cu_tokens, (n_seqs + 1,))
-    max_pages = _table(block_table, n_seqs)
     dev = _here(xk, xv, k._keep[0], v_keep, block_table, cu_tokens, pos0, status)
     rc = _lib.hqmq_paged_write(
-        k._ref, v_ref, xk.data_ptr(), _addr(xv), _code(xk), ks[0], ks[1], vs[0], vs[1], xk.shape[0], n_seqs,
+        k._ref, v_ref, xk.data_ptr(), _addr(xv), _code(xk), ks[0], ks[1], vs[0], vs[1], s[0], n_seqs,
         cu_tokens.data_ptr(), pos0.data_ptr(), block_table.data_ptr(), max_pages, _addr(status), _on(stream, dev))
     if rc:
         _check("hqmq_paged_write", rc)
