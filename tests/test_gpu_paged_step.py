@@ -259,3 +259,39 @@ def test_two_streams_and_two_graphs():
     for layer, (o, lse) in zip(layers, want):
         assert torch.equal(layer.o, o) and torch.equal(layer.lse, lse)
         assert hqmq.read_status(layer.status)["flags"] & ~hqmq.FLAG_OUTLIER_OVERFLOW == 0
+
+
+def test_pages_past_32_bit_offsets():
+    """The same tokens in the first pages of a small pool and in the last pages of one whose words and radii each
+    pass 2^32 bytes (12 GB, only the used pages are touched): the same pages, tokens and attention, bit for bit."""
+    H, page, S, cap, lens = 16, 256, 32, 512, [300, 5, 257]
+    big = (1 << 32) // (H * page * 40) + 3                                # 40 bytes of words, 64 of radii
+    cb = torch.from_numpy(P.make_codebook(np.random.default_rng(8), H, S)).cuda()
+    thr = torch.full((H,), 4.0, device="cuda")
+    table = np.array([[0, 1], [2, -1], [3, 4]], np.int32)
+    cu_d, pos_d, len_d = cuda_ints(np.concatenate([[0], np.cumsum(lens)]), [0, 0, 0], lens)
+    x = torch.randn(sum(lens), H, D, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    q = torch.randn(3, 2 * H, D, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    got = []
+    for n, shift in ((5, 0), (big, big - 5)):
+        words = torch.empty(n, H, page, 10, dtype=torch.int32, device="cuda")
+        radius = torch.empty(n, H, page, 32, dtype=torch.int16, device="cuda")
+        flags = torch.empty(n, H, page, dtype=torch.int32, device="cuda")
+        val = torch.empty(n, H, cap, 4, dtype=torch.int16, device="cuda")
+        for t in (words, radius, flags, val):
+            t[shift:].zero_()
+        kp = hqmq.kv_pages(words, radius, cb, flags, val, thr)
+        t_d = cuda_ints(np.where(table < 0, -1, table + shift))[0]
+        status = hqmq.new_status()
+        hqmq.hqmq_paged_write(x, None, kp, None, t_d, cu_d, pos_d, status=status)
+        y = torch.zeros(3, H, max(lens), D, dtype=BF, device="cuda")
+        hqmq.hqmq_paged_read(kp, t_d, len_d, y, status=status)
+        o = torch.empty(3, 2 * H, D, device="cuda")
+        hqmq.hqmq_attention_paged(q, kp, kp, t_d, len_d, o, hqmq.alloc_attention_paged_ws(3, 2 * H, kp, 2, 256),
+                                  prefix_table=t_d[0, :1].contiguous(), prefix_len=256, status=status)
+        assert hqmq.read_status(status)["flags"] == 0
+        got.append([t[shift:].clone() for t in (words, radius, flags, val)] + [y, o])
+        del words, radius, flags, val, kp
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool(got[0][4].abs().sum() > 0) and bool(got[0][5].isfinite().all())
