@@ -1,0 +1,98 @@
+"""hqmq_paged_read and hqmq_paged_write where a CTA takes many tokens: reads of
+64, 128 and 256 tokens a CTA (the call halves 256 until there are 296 CTAs),
+whose slots are scanned over several warps and pages, and writes of several
+blocks of 64 tokens in one page through the search tables, whose slots carry
+from block to block.  Everything is compared bit for bit (tests/_paged.py,
+tests/_paged_fast.py)."""
+import numpy as np
+import pytest
+import torch
+
+import _paged as P
+import _paged_fast as F
+from test_gpu_paged_cache import cuda_ints, layout, tokens
+from kv_cache_quantization_hqmq_b200 import hqmq
+
+pytestmark = pytest.mark.gpu
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+
+def read_span(T, heads, n_seqs):
+    span = 256
+    while span > 32 and -(-T // span) * heads * n_seqs < 296:
+        span //= 2
+    return span
+
+
+@pytest.mark.parametrize("span,heads,lens,T", [
+    (64, 8, [1200, 611], 1203), (128, 16, [1200, 0, 129], 1200), (256, 32, [1500, 700, 1, 257], 1500)])
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("S,full", [(32, False), (8, True)])
+def test_reads_of_many_tokens_a_cta(span, heads, lens, T, page, S, full):
+    """Dense flagged chunks, with slots for all of them or (full) for a part of a page's."""
+    assert read_span(T, heads, len(lens)) == span
+    rng = np.random.default_rng(span + page)
+    table, n = layout(rng, lens, page)
+    pool = P.empty_pool(rng, n, heads, page, S, 3 * page if full else 32 * page)
+    pool["flags"] &= rng.integers(0, 1 << 32, pool["flags"].shape, dtype=np.uint64).astype(np.uint32)
+    pool["flags"] &= rng.integers(0, 1 << 32, pool["flags"].shape, dtype=np.uint64).astype(np.uint32)
+    pool["words"] = F.pack_all(rng.integers(0, 24 * S, pool["radius"].shape), pool["words"].shape[3])
+    used = np.bitwise_count(pool["flags"]).sum(-1) if hasattr(np, "bitwise_count") else None
+    assert used is None or bool((used > pool["cap"]).any()) == full
+    kp, _ = P.upload(pool)
+    t_d, len_d = cuda_ints(table, lens)
+    vals = F.values(pool)
+    for out in (torch.float32, torch.bfloat16):
+        status = hqmq.new_status()
+        y = torch.full((len(lens), heads, T, 128), 7.0, dtype=out, device="cuda")
+        hqmq.hqmq_paged_read(kp, t_d, len_d, y, status=status)
+        for b, m in enumerate(lens):
+            want = np.ascontiguousarray(F.dense(vals, table[b], m))
+            got = y[b].float().cpu().numpy()
+            np.testing.assert_array_equal(got[:, :m], P.bf16(want) if out == torch.bfloat16 else want)
+            assert (got[:, m:] == 7).all()
+        assert hqmq.read_status(status)["flags"] == 0
+
+
+def test_reads_with_bad_pages_inside_a_cta():
+    """A bad page among the several of a CTA: its rows stay, and the next page's slots start anew."""
+    rng = np.random.default_rng(31)
+    lens, heads, page = [900, 800, 512], 40, 64
+    assert read_span(900, heads, 3) == 256
+    table, n = layout(rng, lens, page)
+    pool = F.filled_pool(rng, n, heads, page, 32, 40)
+    vals = F.values(pool)
+    table[0, 1], table[0, 5], table[1, 0], table[2, 7] = -1, n, -7, 1 << 30
+    kp, _ = P.upload(pool)
+    status = hqmq.new_status()
+    y = torch.full((3, heads, 900, 128), 7.0, device="cuda")
+    hqmq.hqmq_paged_read(kp, *cuda_ints(table, lens), y, status=status)
+    got = y.cpu().numpy()
+    for b, m in enumerate(lens):
+        ok = ((table[b] >= 0) & (table[b] < n)).repeat(page)[:m]
+        want = F.dense(vals, np.where((table[b] >= 0) & (table[b] < n), table[b], 0), m)
+        np.testing.assert_array_equal(got[b][:, :m][:, ok], want[:, ok])
+        assert (got[b][:, :m][:, ~ok] == 7).all() and (got[b][:, m:] == 7).all()
+    assert hqmq.read_status(status)["flags"] == hqmq.FLAG_BAD_PAGE
+
+
+@pytest.mark.parametrize("S,page,row0,new,cap", [
+    (32, 256, 0, [256], 8192), (32, 256, 37, [219], 8192), (8, 256, 0, [240], 700),      # slots run out in a later block
+    (8, 128, 37, [300, 91], 60), (32, 128, 0, [128, 120], 4096), (48, 256, 5, [251, 200], 1500)])
+def test_writes_of_many_tokens_to_a_page(S, page, row0, new, cap):
+    rng = np.random.default_rng(S + page + row0)
+    old = [row0] * len(new)
+    table, n_pages = layout(rng, [a + b for a, b in zip(old, new)], page)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    pool = P.empty_pool(rng, n_pages, 1, page, S, cap, thr=2.2)                          # about a third is above 2.2
+    pool["flags"] &= np.uint32(0x00400010)
+    x, xf = tokens(rng, int(cu[-1]), 1, torch.bfloat16)
+    status = hqmq.new_status()
+    kp, t = P.upload(pool, P.search_tables(pool["cb"]))
+    hqmq.hqmq_paged_write(x.cuda(), None, kp, None, *cuda_ints(table, cu, old), status=status)
+    tally = P.write(pool, xf, table, cu, old)
+    P.assert_pools_equal(t, pool)
+    st = hqmq.read_status(status)
+    assert st["n_outliers"] == tally["n_outliers"] > 20 * len(new)
+    assert bool(st["flags"] & hqmq.FLAG_OUTLIER_OVERFLOW) == (tally["overflow"] > 0) == (cap in (60, 700, 1500))
