@@ -620,9 +620,9 @@ HQMQ_API uint64_t hqmq_attention_paged_workspace_size(int B, int Hq, int Hk, int
  *   o[b][h] = sum_t softmax_t(scale <q[b][h], K^_t>) V^_t,   KV head h / G,
  * with K^, V^ the bf16 values of hqmq_paged_read and G = Hq / heads <= 16.
  * bf16 products accumulated in fp32; softmax in base 2 with a running
- * maximum, its sum taken in fp32; the weights enter P V as bf16 terms whose
- * sum is fp32 accurate (three) if out_dtype is HQMQ_F32, and rounded to one
- * bf16 term (relative 2^-9, as the output's own rounding) if it is HQMQ_BF16.
+ * maximum, its sum taken in fp32; the weights enter P V as bf16 terms: three
+ * if out_dtype is HQMQ_F32 (2^-24 of a weight is left), two if it is HQMQ_BF16
+ * (2^-17, as in hqmq_attention_decode, below the output's own rounding).
  * No token at all gives o = 0 and lse = -inf; tokens of bad pages are left
  * out; an index >= 24 S reads as the zero codeword.  d_seq_len is clamped to
  * [0, max_pages page_size].

@@ -25,9 +25,10 @@
 //   * two warps issue the products (tcgen05.mma, 128 rows, accumulators
 //     and the A operands Q and P in tensor memory);
 //   * 4 MT softmax warps, a thread per row: scores from tensor memory, online
-//     softmax in base 2, P back as bf16: one term for bf16 outputs (its
-//     2^-9 is the output's own rounding), three for fp32 outputs (2^-24, so
-//     that fp32 outputs are fp32 accurate; two would leave 2^-17).  The sum is
+//     softmax in base 2, P back as bf16: two terms for bf16 outputs (they leave
+//     2^-17 of a weight, so that the output's own half step, 2^-8, is all that
+//     shows; one term leaves as much as that step), three for fp32 outputs
+//     (2^-24, so that fp32 outputs are fp32 accurate).  The sum is
 //     taken in fp32 before the rounding.  The reference maximum moves only when a row's
 //     maximum has grown by more than 2^8 (then O is rescaled in tensor
 //     memory): weights up to 2^8 lose nothing in floating point.
@@ -36,16 +37,17 @@
 // (the others get weight 0) and keeps a partial of its own.
 //
 // MT = 2 (bf16 outputs, more than 128 rows over the prefix) decodes a tile once
-// for 256 rows instead of twice: what bounds it is not the products (1024
-// clocks a tile at 16384 multiply-adds a clock) but the chain scores -> softmax
+// for 256 rows instead of twice: what bounds it is not the products (1536
+// clocks a tile at 4096 multiply-adds a clock) but the chain scores -> softmax
 // -> P V -> next scores of its two half-tile buffers, beside which the
-// producers' decoding fits.  Measured (bf16, S = 32, 8 KV heads, pages of 64):
-// 32 sequences of 1000 tokens behind 131072: 204 us, 138 GFLOP at 675 TFLOP/s,
-// 272 MB of codes (an earlier step, at 228: with the decoding left out 189 us, with decoding, softmax
-// arithmetic and products left out 133 us, the hand-overs' latency).  A score
+// producers' decoding fits.  Measured (device time, calls back to back; bf16, S = 32, 8 KV heads, pages of
+// 64): 32 sequences of up to 1000 tokens behind 131072: 233 us, 138 GFLOP at
+// 592 TFLOP/s, 272 MB of codes (272 us as a call with cold caches).  With one
+// term a weight it takes 204 us, and of the variants tried at that stage a score
 // step of 64 tokens without double buffers took 235 us, one warp for all
 // products 259 us.  One group of 128 rows (MT = 1) spends its time on the
-// pieces' ends and the decoding: 16 sequences of 500 tokens behind 8191: 31 us.
+// pieces' ends and the decoding: 16 sequences of up to 500 tokens behind 8191:
+// 32 us.
 //
 // Every wait is bounded; one that runs out sets HQMQ_FLAG_TIMEOUT.
 #include "paged.cuh"
@@ -218,7 +220,7 @@ template <int MT, int NT> struct Tmem {
     __host__ __device__ static constexpr uint32_t s(int i) { return MT * 192 + i * 64; }
     __host__ __device__ static constexpr uint32_t half(int g, int h) { return MT * 192 + g * 64 + h * 32; }
     __host__ __device__ static constexpr uint32_t p(int i) { return MT == 1 ? 320 + i * P_COLS : 128 + i * 64; }
-    static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64 && NT == 1, "tensor memory");
+    static_assert(MT == 1 ? 320 + 2 * P_COLS <= 512 : P_COLS <= 64, "tensor memory");
 };
 // Where term t of the weights of tokens 16 k .. 16 k + 15 lies in P.
 template <int NT> __host__ __device__ constexpr uint32_t p_col(int k, int t) { return (k >> 1) * 16 * NT + t * 16 + (k & 1) * 8; }
@@ -1222,8 +1224,9 @@ struct PartPlan {
 inline PartPlan part_plan(int B, int Hq, int Hk, int max_tokens, int prefix_len, int out_dtype) {
     PartPlan p;
     const int64_t rows = (int64_t)B * (Hq / Hk);
-    // fp32 outputs take three terms of P, which leaves tensor memory for one group of rows.  (256 rows over
-    // 131072 tokens, bf16: 215 us as two groups at once, 304 as one after the other.)
+    // fp32 outputs take three terms of P, which leaves tensor memory for one group of rows.  (256 rows of 32
+    // sequences with up to 1000 own tokens, bf16, two groups at once and one after the other: behind 131072
+    // tokens 234 and 302 us, behind 32768 100 and 106, behind 8191 62 and 57.)
     p.mt = prefix_len > 0 && rows > 128 && out_dtype == HQMQ_BF16 ? 2 : 1;
     p.row_tiles = prefix_len > 0 ? (int)((rows + 128 * p.mt - 1) / (128 * p.mt)) : 0;
     p.prefix_slot_rows = rows <= PA_REP_ROWS ? (int)(4 * rows) : 128 * p.mt;
@@ -1310,6 +1313,6 @@ extern "C" int hqmq_launch_attention_paged(const uint16_t *q, const hqmq_kv_page
                                  (int64_t)B * (((int64_t)max_pages * k->page_size + PA_TILE - 1) / PA_TILE));
     const int ctas = (int)(most < PA_CTAS ? most : PA_CTAS);
     if (out_dtype == HQMQ_F32) return launch_paged_attn<1, 3>(a, ctas, o, out_dtype, lse, stream);
-    return p.mt == 2 ? launch_paged_attn<2, 1>(a, ctas, o, out_dtype, lse, stream)
-                     : launch_paged_attn<1, 1>(a, ctas, o, out_dtype, lse, stream);
+    return p.mt == 2 ? launch_paged_attn<2, 2>(a, ctas, o, out_dtype, lse, stream)
+                     : launch_paged_attn<1, 2>(a, ctas, o, out_dtype, lse, stream);
 }

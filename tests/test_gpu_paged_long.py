@@ -3,7 +3,9 @@
 tile to tile, and shares pass from segment to segment, from two groups of rows
 to replicated ones and back, and from head to head.  The bounds are those of
 tests/_paged_fast.py, element by element; a weight enters P V as three bf16
-terms for fp32 outputs, which leave 2^-24 of it."""
+terms for fp32 outputs (2^-24 left) and as two for bf16 outputs (a term leaves
+at most half a step of its value: 2^-8, and the second of what is left, which
+is below a power of two, 2^-9 more: 2^-17)."""
 import numpy as np
 import pytest
 import torch
@@ -16,7 +18,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 BF, F32 = torch.bfloat16, torch.float32
-WEIGHT = {F32: 2.0 ** -24}
+WEIGHT = {F32: 2.0 ** -24, BF: 2.0 ** -17}
 
 
 def tiles(x, out):
@@ -45,13 +47,24 @@ CASES = {
     "mixed": dict(B=17, Hk=6, G=8, page=128, S=8, cap=0, Sv=32, capv=200, lens=[90] * 17, prefix=5000)}
 
 
-@pytest.mark.parametrize("out", [F32])
+@pytest.mark.parametrize("out", [F32, BF])
 @pytest.mark.parametrize("case", CASES)
 def test_many_tiles_a_cta(case, out):
     x = F.Batch(len(case), **CASES[case])
     assert tiles(x, out) > 4 * 148
     o, lse = x.call(out)
     print("[paged attention, long] %s: largest error / bound %.3g" % (case, x.check(o, lse, WEIGHT[out])))
+
+
+@pytest.mark.parametrize("B,Hk,G,lens,prefix", [
+    (3, 2, 8, [500, 20, 0], 700), (10, 2, 8, [60] * 10, 900), (33, 2, 8, [1, 70, 0] * 11, 1000)])
+def test_bf16_outputs_are_the_fp32_ones_rounded(B, Hk, G, lens, prefix):
+    """Apart from the output's own rounding, a bf16 output is as good as two terms a weight: 2^-17."""
+    x = F.Batch(B, B, Hk, G, 64, 32, 128, lens, prefix)
+    o32, lse = x.call(F32)
+    o16, lse16 = x.call(BF)
+    x.check(o32, lse, WEIGHT[F32])
+    x.check(o16, lse16, WEIGHT[BF])
 
 
 def sawtooth(period, rise):
@@ -71,7 +84,7 @@ def sawtooth(period, rise):
     return make
 
 
-@pytest.mark.parametrize("out", [F32])
+@pytest.mark.parametrize("out", [F32, BF])
 @pytest.mark.parametrize("B,Hk,G,lens,prefix", [
     (1, 4, 1, [0], 40000), (2, 8, 2, [20000, 17000], 0), (8, 4, 8, [100] * 8, 30000), (25, 4, 8, [70] * 25, 30000)])
 def test_rising_scores_move_the_maximum_again_and_again(B, Hk, G, lens, prefix, out):
