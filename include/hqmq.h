@@ -529,8 +529,10 @@ typedef struct {
     int out_cap;                  /* slots of a (page, head), 1 .. 32 page_size; ignored without flags */
 } hqmq_kv_pages;
 
-/* A page id outside [0, n_pages), a position below 0 or a position past the
- * block table's last page: the tokens concerned are left out. */
+/* A page id outside [0, n_pages) or a position past the block table's last
+ * page: the tokens concerned are left out.  A first position below 0
+ * (hqmq_paged_write's d_pos0): all new tokens of that sequence are left out,
+ * those at positions from 0 on too, since a start below 0 names no place. */
 #define HQMQ_FLAG_BAD_PAGE 32u
 
 /* A bounded wait inside hqmq_attention_paged ran out (the outputs are then

@@ -96,3 +96,51 @@ def test_writes_of_many_tokens_to_a_page(S, page, row0, new, cap):
     st = hqmq.read_status(status)
     assert st["n_outliers"] == tally["n_outliers"] > 20 * len(new)
     assert bool(st["flags"] & hqmq.FLAG_OUTLIER_OVERFLOW) == (tally["overflow"] > 0) == (cap in (60, 700, 1500))
+
+
+@pytest.mark.parametrize("new,tables", [(3, False), (80, True)])
+def test_a_start_below_zero_leaves_the_whole_sequence_out(new, tables):
+    """As the header says: also the tokens whose positions would be 0 and more; the neighbours are written."""
+    rng = np.random.default_rng(41)
+    table, n_pages = layout(rng, [new, new, new], 16)
+    cu, pos0 = [0, new, 2 * new, 3 * new], [0, -1, 0]
+    pool = P.empty_pool(rng, n_pages, 2, 16, 32, 24)
+    x, xf = tokens(rng, 3 * new, 2, torch.bfloat16)
+    status = hqmq.new_status()
+    kp, t = P.upload(pool, P.search_tables(pool["cb"]) if tables else None)
+    hqmq.hqmq_paged_write(x.cuda(), None, kp, None, *cuda_ints(table, cu, pos0), status=status)
+    assert P.write(pool, xf, table, cu, pos0)["bad"] == new
+    P.assert_pools_equal(t, pool)
+    assert hqmq.read_status(status)["flags"] & hqmq.FLAG_BAD_PAGE
+
+
+def test_special_values_through_the_tables():
+    """Zeros, NaN, infinities, norms beyond fp16 and fp32 and next to their ends, among runs long enough
+    for the search tables."""
+    rng = np.random.default_rng(42)
+    x = rng.standard_normal((70, 2, 128)).astype(np.float32)
+    x[3, 0] = 0
+    x[5, 1, 4] = np.nan
+    x[8, 0, 9] = np.inf
+    x[11, 1, 8:12] = [1e5, -7e4, 3, 0]
+    x[20, 0, :4] = [3e38, 3e38, 0, 0]
+    x[21, 0, :8] = [1.8e19, 0, 0, 0, 9e18, -9e18, 9e18, 9e18]          # squares next to the largest fp32
+    x[22, 1, :4] = [1e-30, 0, 0, 0]
+    x[23, 1, :12] = [2e-20, -3e-20, 1e-21, 0, 4e-23, 0, 0, 0, 0, 0, -3e-22, 1e-45]
+    x[30, 1, 12:16] = [-np.inf, np.nan, 1, 1]
+    x[40, 0, :8] = [1, 0, 0, 0, 0.5, 0.5, 0.5, -0.5]
+    x[64:, 1, 64:] *= 1e4
+    for S, cap in ((32, 0), (32, 40), (8, 400), (48, 100)):
+        table, n_pages = layout(rng, [70], 64)
+        pool = P.empty_pool(rng, n_pages, 2, 64, S, cap)
+        status = hqmq.new_status()
+        want = P.copy_pool(pool)
+        kp, t = P.upload(pool, P.search_tables(pool["cb"]))
+        hqmq.hqmq_paged_write(torch.from_numpy(x).cuda(), None, kp, None, *cuda_ints(table, [0, 70], [0]), status=status)
+        tally = P.write(want, x, table, [0, 70], [0])
+        P.assert_pools_equal(t, {**want, "val": None})
+        if cap:                        # NaN payloads aside, the stored values too
+            np.testing.assert_array_equal(t["val"].cpu().numpy().view(np.float16), want["val"].view(np.float16))
+        st = hqmq.read_status(status)
+        assert (st["n_outliers"], st["n_saturated"], st["n_nonfinite"]) == \
+            (tally["n_outliers"], tally["n_saturated"], tally["n_nonfinite"])
