@@ -30,8 +30,7 @@ namespace hqmq {
 
 constexpr int PW_LOOP_WARPS = 4, PW_TABLE_WARPS = 8;
 constexpr int PW_TOKENS = 8;                  // tokens of a warp of the table kernel, at most
-constexpr int PW_SEARCH_FROM = 8;             // tokens of a sequence, on average
-constexpr uint32_t PW_SEARCH_S = 8;
+constexpr uint32_t PW_SEARCH_S = 8;           // the smallest codebook that is searched through its tables
 constexpr int PW_RUNS_FROM = 4;               // tokens of a sequence, on average
 
 struct WriteArgs {
@@ -577,9 +576,16 @@ extern "C" int hqmq_launch_paged_write(const hqmq_kv_pages *k, const hqmq_kv_pag
     const uint32_t S = v && v->S > k->S ? v->S : k->S;
     // the tables pay for runs of some tokens (their codewords have to be brought to shared memory) and
     // codebooks of some size (the loop costs about 25 instructions a secondary).  8 heads, K and V, loop and
-    // table: 4096 tokens, pages of 64: S = 32 131 and 51 us, S = 8 69 and 41; 32 sequences of 24 tokens at
-    // S = 8: 15.5 and 15.2 us in pages of 64, 13.9 and 15.2 in pages of 16
-    const bool search = k->table && (!v || v->table) && n_tokens >= PW_SEARCH_FROM * n_seqs && S >= PW_SEARCH_S;
+    // table, us: 4096 tokens, pages of 64: S = 32 131 and 51, S = 8 69 and 41; 768 tokens in sequences of
+    //            pages of 16, 8 tokens  16 tokens  24 tokens   of 64, 8 tokens  16 tokens  24 tokens
+    //   S = 8          23.3 31.2  21.3 23.1  19.6 20.3          21.1 26.8  20.4 19.0  18.4 18.2
+    //   S = 16         27.4 33.7  25.6 24.4  24.5 21.9          24.9 29.3  25.1 21.6  23.5 19.5
+    //   S = 32         35.2 40.1  34.9 30.2  33.1 26.4          32.8 35.8  33.9 25.4  33.0 23.5
+    // One kernel takes the whole call, by the average: lengths stay on the device.  A batch that mixes single
+    // tokens with a long run pays for it (S = 32, pages of 64, tables; the two parts as calls of their own): 64
+    // single tokens and a run of 512 take 38 us (8 + 20), 256 and a run of 1024 106 us (27 + 25).
+    const int search_from = S < 16 ? 24 : 16;
+    const bool search = k->table && (!v || v->table) && S >= PW_SEARCH_S && n_tokens >= search_from * n_seqs;
     const size_t smem = search ? (size_t)(24 * S + 1) * sizeof(float4) : 0;
     const dim3 grid((unsigned)runs, (unsigned)k->heads, (unsigned)roles);
     const uint32_t bb = v && bv != bk ? 0 : bk;
