@@ -8,11 +8,12 @@
 // contiguous.  A token's addresses are worked out once, by the thread that
 // looked its page up, and the loads of four steps are issued without a branch
 // before the first is used.  32768 tokens of 8 heads, S = 32, to bf16 (97 MB)
-// take 27 us, 3.6 TB/s: half the rate of a copy.  The chain length -> page ->
-// flags -> codes of a CTA's start and the shared-memory pipe (a codeword per
-// chunk, with bank conflicts) share the rest; more table copies (4: 30 us, they
-// take L1's room), eight steps in flight (30) and CTAs that stay for several
-// rounds (27) gained nothing.
+// take 26.7 us, 3.6 TB/s (to fp32, 164 MB, 39.4 us; 131072 tokens 99 and 134 us,
+// 3.9 and 4.9 TB/s): half the rate of a copy and more.  The chain length -> page
+// -> flags -> codes of a CTA's start and the shared-memory pipe (a codeword per
+// chunk, with bank conflicts) share the rest; other numbers of table copies
+// (4: 32 us, they take L1's room; 1: 26.7), eight steps in flight (30) and CTAs
+// that stay for several rounds (27) gained nothing.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -46,8 +47,8 @@ __device__ __forceinline__ float4 half4(uint2 h) {
 }
 
 // CPL: chunks a lane takes (2: bf16, 1: fp32); a warp's step covers CPL tokens.
-// BB: bits of an index, if known to the compiler.
-template <int CPL, int BB> __global__ void __launch_bounds__(PR_THREADS, 4) k_paged_read(ReadArgs a) {
+// (Index widths known to the compiler gain nothing: 26.9 us.)
+template <int CPL> __global__ void __launch_bounds__(PR_THREADS, 4) k_paged_read(ReadArgs a) {
     extern __shared__ float4 s_tab[];         // [24 S + 1][PR_COPIES]
     __shared__ ReadTok s_tok[PR_THREADS];
     __shared__ uint32_t s_sum[PR_WARPS];
@@ -119,7 +120,7 @@ template <int CPL, int BB> __global__ void __launch_bounds__(PR_THREADS, 4) k_pa
     __syncthreads();
 
     constexpr int STEPS = 4;                  // loads in flight: STEPS tokens a lane
-    const uint32_t b = BB ? BB : p.b;
+    const uint32_t b = p.b;
     const int sub = CPL == 2 ? lane >> 4 : 0, c0 = CPL == 2 ? 2 * (lane & 15) : lane;
     const uint32_t bit = (uint32_t)c0 * b, wi = bit >> 5, sh = bit & 31u, mask = (1u << b) - 1u;
     const bool two = wi + 1 < b;              // (CPL b bits lie in one or two words: b <= 11)
@@ -211,8 +212,7 @@ extern "C" int hqmq_launch_paged_read(const hqmq_kv_pages *c, uint32_t b, int n_
     a.span = 256;
     while (a.span > 32 && (int64_t)((T + a.span - 1) / a.span) * c->heads * n_seqs < 2 * 148) a.span /= 2;
     const size_t smem = (size_t)(24 * c->S + 1) * PR_COPIES * sizeof(float4);
-    auto kern = out_dtype == HQMQ_BF16 ? (b == 8 ? k_paged_read<2, 8> : b == 10 ? k_paged_read<2, 10> : k_paged_read<2, 0>)
-                                       : (b == 8 ? k_paged_read<1, 8> : b == 10 ? k_paged_read<1, 10> : k_paged_read<1, 0>);
+    auto kern = out_dtype == HQMQ_BF16 ? k_paged_read<2> : k_paged_read<1>;
     const dim3 grid((unsigned)((T + a.span - 1) / a.span), (unsigned)c->heads, (unsigned)n_seqs);
     return launch_pdl(kern, grid, dim3(PR_THREADS), smem, stream, a) == cudaSuccess ? HQMQ_OK : HQMQ_ERR_CUDA;
 }
