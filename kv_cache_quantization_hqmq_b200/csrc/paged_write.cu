@@ -265,7 +265,7 @@ __device__ __forceinline__ uint32_t pick_candidate(const Token &t, uint4 rec, ui
 // A stored token's index words again, by the loop over the codebook: for what the table's candidates in
 // fp32 could not tell, and for cells with more candidates than a record holds.  Out of line and after the
 // warp's other tokens, so that it costs them no registers.
-template <int DT, int BB>
+template <int DT>
 __device__ __noinline__ void settle_token(const PagesDev &p, const char *x, size_t at, const float4 *s_cb, int lane) {
     RawChunk<DT> c;
     c.load(x, lane);
@@ -277,7 +277,7 @@ __device__ __noinline__ void settle_token(const PagesDev &p, const char *x, size
         idx = settle_index(t.x0, t.x1, t.x2, t.x3, s_cb, p.S,
                            scan_secondaries(t.x0, t.x1, t.x2, t.x3, s_cb, 0, p.S));
     __syncwarp();
-    pack_group32<BB>(idx, p.b, lane, pack_const(p.b, lane), p.words + at * p.b);
+    pack_group32<0>(idx, p.b, lane, pack_const(p.b, lane), p.words + at * p.b);
 }
 
 struct Tally {
@@ -353,7 +353,7 @@ __device__ __forceinline__ void store_token(Token &t, const PagesDev &p, size_t 
     p.radius[at * PG_CHUNKS + lane] = rh;
 }
 
-template <int DT, int BB>
+template <int DT>
 __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 4) k_paged_write_table(const __grid_constant__ WriteArgs a) {
     constexpr int WARPS = PW_TABLE_WARPS, THREADS = WARPS * 32;
     extern __shared__ float4 s_tab[];         // 24 S + 1 codewords
@@ -444,13 +444,13 @@ __global__ void __launch_bounds__(PW_TABLE_WARPS * 32, 4) k_paged_write_table(co
                 bool clear;
                 const uint32_t idx = pick_candidate(ks, rs, kmax, s_tab, clear);
                 if (!__all_sync(FULL, clear)) unclear |= 1u << (i - 1);
-                pack_group32<BB>(idx, p.b, lane, pc, p.words + (at - 1) * p.b);
+                pack_group32<0>(idx, p.b, lane, pc, p.words + (at - 1) * p.b);
             }
         }
         __syncwarp();
         for (; unclear; unclear &= unclear - 1u) {
             const int i = __ffs(unclear) - 1;
-            settle_token<DT, BB>(p, pl.x + (t0 + i) * xt, pl.at0 + t0 + i, s_cb, lane);
+            settle_token<DT>(p, pl.x + (t0 + i) * xt, pl.at0 + t0 + i, s_cb, lane);
         }
     }
     n.add_to(a.st_out, lane);
@@ -533,9 +533,11 @@ __global__ void __launch_bounds__(PW_LOOP_WARPS * 32, CTAS) k_paged_write_loop(c
 
 using WriteKernel = void (*)(WriteArgs);
 template <int DT, int BB> WriteKernel write_kernel_b(bool search, bool runs_of_some) {
-    return search ? k_paged_write_table<DT, BB> : runs_of_some ? k_paged_write_loop<DT, BB, 5> : k_paged_write_loop<DT, BB, 7>;
+    return search ? k_paged_write_table<DT> : runs_of_some ? k_paged_write_loop<DT, BB, 5> : k_paged_write_loop<DT, BB, 7>;
 }
-// bb: bits of the indices of K and V, where compiled for (S = 6 .. 10 and 22 .. 42), else 0.
+// bb: bits of the indices of K and V where the loop is compiled for them (S = 6 .. 10 and 22 .. 42), else 0.
+// Steps of one token of 64 sequences, 8 heads, fp32, with the width at run time and compiled in: S = 32 8.4
+// and 7.8 us, S = 8 6.1 and 5.8; the table kernel gains nothing by it (4096 tokens 52.4 and 52.8 us).
 template <int DT> WriteKernel write_kernel(uint32_t bb, bool search, bool runs_of_some) {
     return bb == 8    ? write_kernel_b<DT, 8>(search, runs_of_some)
            : bb == 10 ? write_kernel_b<DT, 10>(search, runs_of_some)
