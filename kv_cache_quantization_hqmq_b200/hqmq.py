@@ -409,6 +409,9 @@ _DTYPE_CODE = {torch.bfloat16: HQMQ_BF16, torch.float32: HQMQ_F32}
 # torch.cuda.current_device without its check that CUDA is up: tensors on a device are there already, and
 # without any the answer does not match theirs
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# the current stream's handle without a Stream object (None: a torch that has no such shortcut)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_INT_MAX = 0x7FFFFFFF                                     # ctypes cuts larger numbers off
 
 
 def _here(*tensors):
@@ -424,7 +427,7 @@ def _here(*tensors):
 def _on(stream, dev):
     """The stream's handle; None: torch's current stream of the device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     return _stream(stream)
 
 
@@ -438,16 +441,16 @@ def _addr(t):
 
 
 def _ints(name, t, shape):
-    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor of shape %s, got %s %s"
-                         % (name, shape, t.dtype, tuple(t.shape)))
+    if t is None or t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s, got %s"
+                         % (name, tuple(shape), t if t is None else (t.dtype, tuple(t.shape))))
 
 
 def _table(t, n_seqs=None, name="block_table"):
-    s = t.shape
+    s = () if t is None else t.shape
     if len(s) != 2 or (n_seqs is not None and s[0] != n_seqs) or t.dtype is not _I32 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 [n_seqs, max_pages], got %s %s"
-                         % (name, t.dtype, tuple(s)))
+        raise ValueError("%s must be a contiguous int32 [n_seqs, max_pages], got %s"
+                         % (name, t if t is None else (t.dtype, tuple(s))))
     return s[1]
 
 
@@ -583,11 +586,11 @@ def hqmq_paged_write(xk, xv, k, v, block_table, cu_tokens, pos0, status=None, st
     int32 [n_seqs].  xv and v may be None."""
     s, ks, vs, v_ref, v_keep = xk.shape, xk.stride(), (0, 0, 1), None, None
     if v is not None:
-        if xv.shape != s or xv.dtype is not xk.dtype:
-            raise ValueError("xk and xv must agree in shape and dtype")
+        if xv is None or xv.shape != s or xv.dtype is not xk.dtype:
+            raise ValueError("xk and xv must agree in shape and dtype (and xv be there where v is)")
         vs, v_ref, v_keep = xv.stride(), v._ref, v._keep[0]
-    if len(s) != 3 or s[1] != k.heads or s[2] != 128 or ks[2] != 1 or vs[2] != 1:
-        raise ValueError("new tokens are [n_tokens, %d, 128] with a contiguous last dimension, got "
+    if len(s) != 3 or s[1] != k.heads or s[2] != 128 or ks[2] != 1 or vs[2] != 1 or s[0] > _INT_MAX:
+        raise ValueError("new tokens are [n_tokens < 2^31, %d, 128] with a contiguous last dimension, got "
                          "%s" % (k.heads, tuple(s)))
     max_pages = _table(block_table)
     n_seqs = block_table.shape[0]
@@ -618,6 +621,8 @@ def hqmq_paged_read(c, block_table, seq_len, y, status=None, stream=None):
 
 
 def hqmq_attention_paged_workspace_size(B, Hq, Hk, max_tokens, prefix_len=0):
+    if max(B, Hq, Hk, max_tokens, prefix_len) > _INT_MAX:
+        return 0
     return int(_lib.hqmq_attention_paged_workspace_size(B, Hq, Hk, max_tokens, prefix_len))
 
 
@@ -647,6 +652,8 @@ def hqmq_attention_paged(q, k, v, block_table, seq_len, o, ws, prefix_table=None
         _ints("seq_len", seq_len, (B,))
     if prefix_len > 0:
         need = (prefix_len + k.page_size - 1) // k.page_size
+        if prefix_len > _INT_MAX:
+            raise ValueError("prefix_len must be below 2^31, got %d" % prefix_len)
         if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
             raise ValueError("prefix_table must hold the prefix's %d pages" % need)
         _ints("prefix_table", prefix_table, prefix_table.shape)
