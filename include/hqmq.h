@@ -584,10 +584,13 @@ HQMQ_API int hqmq_qk_norm_rope(const hqmq_head_view *q, const hqmq_head_view *q_
  *   - radius and index as hqmq_encode; scores within fp32 rounding of each
  *     other are compared in fp64, so the index is the argmax of the exact
  *     scores (ties to the lowest index).
- * The result does not depend on how tokens are split into calls.  Sequences
- * must not share a page that this call writes.  k and v agree in page_size
+ * The result does not depend on how tokens are split into calls.  A page that
+ * this call writes must stand in one entry of the block table only (two runs
+ * written to one page at once mix).  k and v agree in page_size
  * and heads; v may be NULL (d_xv is then ignored).  With search tables
- * (hqmq_make_search_table) longer runs of tokens are searched through them.
+ * (hqmq_make_search_table; hqmq_search_table_bytes, 4 MiB a head, so 64 MiB
+ * for K and V of 8 heads), calls of 16 (S < 16: 24) tokens a sequence and more
+ * are searched through them, S from 8 on; the pages are the same without.
  * d_cu_tokens: int32 [n_seqs + 1], non-decreasing from 0 to n_tokens;
  * d_pos0: int32 [n_seqs].  Data 16-byte aligned, strides multiples of 4
  * elements (bf16) or 4 (fp32).  n_tokens may be 0 (nothing is done). */
@@ -632,8 +635,13 @@ HQMQ_API uint64_t hqmq_attention_paged_workspace_size(int B, int Hq, int Hk, int
  * the result can be joined with attention over tokens held elsewhere.
  * d_q: bf16 [B][Hq][128], 16-byte aligned; d_o: [B][Hq][128] of out_dtype,
  * 16-byte aligned; d_block_table NULL with max_pages 0: the prefix alone.
+ * Stored values are taken as finite or NaN, which is what hqmq_paged_write
+ * leaves: NaN reaches the rows that attend to it, and so does an infinity,
+ * as NaN or infinity.  A row whose every score is -inf (an infinite query)
+ * counts as one without tokens.
  * d_ws: at least hqmq_attention_paged_workspace_size bytes, 256-byte
- * aligned, contents on entry ignored. */
+ * aligned, contents on entry ignored; calls that may overlap on the GPU need
+ * one each. */
 HQMQ_API int hqmq_attention_paged(const uint16_t *d_q, const hqmq_kv_pages *k,
                                   const hqmq_kv_pages *v, int B, int Hq,
                                   const int32_t *d_seq_len, const int32_t *d_block_table,

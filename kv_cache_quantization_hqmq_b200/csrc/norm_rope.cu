@@ -9,9 +9,13 @@
 // rotated with each other (or 16 neighbours, when pairs are neighbours or
 // pass through), LPV lanes a vector: 16-byte accesses, the partner of every
 // element in the same lane, log2(LPV) shuffles for the norm.  It needs R and
-// D - R to be multiples of 16 and 16-byte aligned vectors; k_norm_rope_any
-// (a warp per vector, element by element) takes every other call: 8192 tokens
-// of 40 bf16 heads of 128 take 31 us in the first, 129 us in the second.
+// D - R to be multiples of 16 (a lane's 16 elements rotate or pass through as
+// a whole, in two runs of 8) and 16-byte aligned vectors; k_norm_rope_any
+// (a warp per vector, element by element) takes every other call, four times
+// slower: 8192 tokens of 40 bf16 heads of 128 take 31 us in the first, 129 in
+// the second; heads of 96 28 us with all 96 elements rotated, 104 with 24;
+// heads of 80 25 us with 32 rotated, 98 with 40 (fp32 42 and 109).  A third
+// kernel with runs of 4 would bring those back; none is built.
 #include "hqmq_device.cuh"
 
 namespace hqmq {
@@ -96,7 +100,8 @@ template <> struct Raw8<float> {
 // angles come from shared memory, which leaves 64 registers a thread, and the
 // span is chosen so that the last round of CTAs is nearly full (8192 tokens of
 // 40 heads of 128, bf16, 168 MB: 31 us, 5.4 TB/s; weights in registers and
-// spans of 8: 41 us).
+// spans of 8: 41 us).  fp32 elements take twice the registers: those instances
+// spill 16 to 28 bytes at 64 (the same tokens in fp32, 336 MB: 57 us, 5.8 TB/s).
 template <typename E, int LPV, bool PAIRS>
 __global__ void __launch_bounds__(NR_THREADS, 2) k_norm_rope(const __grid_constant__ NormRopeArgs a, unsigned tokens,
                                                              int span) {

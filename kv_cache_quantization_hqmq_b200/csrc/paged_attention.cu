@@ -41,8 +41,8 @@
 // clocks a tile at 4096 multiply-adds a clock) but the chain scores -> softmax
 // -> P V -> next scores of its two half-tile buffers, beside which the
 // producers' decoding fits.  Measured (device time, calls back to back; bf16, S = 32, 8 KV heads, pages of
-// 64): 32 sequences of up to 1000 tokens behind 131072: 233 us, 138 GFLOP at
-// 592 TFLOP/s, 272 MB of codes (272 us as a call with cold caches).  With one
+// 64): 32 sequences of up to 1000 tokens behind 131072: 230 us, 138 GFLOP at
+// 600 TFLOP/s, 272 MB of codes (269 us as a call with cold caches).  With one
 // term a weight it takes 204 us, and of the variants tried at that stage a score
 // step of 64 tokens without double buffers took 235 us, one warp for all
 // products 259 us.  One group of 128 rows (MT = 1) spends its time on the
@@ -173,7 +173,8 @@ template <int MT> struct Rows {
 
 // Warps: 4 MT softmax, 16 producers, two scouts, two for the products.  The
 // block is launched with REGS a thread, and each group of four warps takes what it
-// needs of their sum.
+// needs of their sum.  (The compiler spills at REGS: 24 to 28 bytes with three terms a weight, 8 to 32 with two
+// groups, none or 4 with one group and two terms.)
 template <int MT> struct Roles {
     static constexpr int SCOUT = 4 * MT + PROD_WARPS, SCOUTS = 2, PRODUCTS = SCOUT + SCOUTS;
     static constexpr int THREADS = (PRODUCTS + 2) * 32;
@@ -1259,7 +1260,9 @@ static int launch_paged_attn(PagedAttnArgs &a, int ctas, void *o, int out_dtype,
     };
     a.copies_k = fits(8, 4) ? 8 : 4;
     a.copies_v = fits(a.copies_k, 8) ? 8 : 4;
-    // the index widths of S = 8 and S = 32 are compiled in
+    // the index widths of S = 8 and S = 32 (6 .. 10, 22 .. 42) are compiled in; others, and K and V that differ,
+    // pick an index's words by selects (S = 32 compiled in and not: 131072 tokens, 256 rows 233 and 276 us; 8191
+    // tokens, 128 rows 32.0 and 35.4)
     if (a.k.b == a.v.b && a.k.b == 8) return launch_paged_attn_b<8, MT, NT>(a, ctas, o, out_dtype, lse, stream);
     if (a.k.b == a.v.b && a.k.b == 10) return launch_paged_attn_b<10, MT, NT>(a, ctas, o, out_dtype, lse, stream);
     return launch_paged_attn_b<0, MT, NT>(a, ctas, o, out_dtype, lse, stream);

@@ -125,3 +125,29 @@ def test_the_same_bits_again():
             y.call(out)
             again = x.call(out)
             assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_rows_whose_scores_are_all_minus_infinity_count_as_empty():
+    """An infinite query against keys of one sign: o = 0 and lse = -inf, as the header says; NaN with the
+    other sign; the neighbours' rows stay."""
+    def pools(rng, n, table, ptable):
+        p = [F.filled_pool(rng, n, 2, 32, 8, 0) for _ in range(2)]
+        p[0]["words"][:] = np.array(P.pack_words([3] * 32, 8), np.uint32)
+        p[0]["radius"][:] = P.f16_bits(np.float32(1.5))
+        pools.sign = np.sign(P.codewords(p[0]["cb"], True)[:, 3, 0]).astype(np.float32)
+        return p
+    x = F.Batch(9, 3, 2, 2, 32, 8, 0, [70, 0, 33], 100, pools=pools)
+    for out in (F32, BF):
+        base = x.q.clone()
+        o0, lse0 = x.call(out)
+        x.q[1, 0] = 0
+        x.q[1, 0, 8] = -float("inf") * float(pools.sign[0])
+        x.q[2, 3] = 0
+        x.q[2, 3, 4] = float("inf") * float(pools.sign[1])
+        o1, lse1 = x.call(out)
+        assert bool((o1[1, 0] == 0).all()) and float(lse1[1, 0]) == -float("inf")
+        assert bool(torch.isnan(o1[2, 3]).all())
+        same = torch.ones(3, 4, dtype=torch.bool, device="cuda")
+        same[1, 0] = same[2, 3] = False
+        assert torch.equal(o0[same], o1[same]) and torch.equal(lse0[same], lse1[same])
+        x.q = base
