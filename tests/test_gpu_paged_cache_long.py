@@ -144,3 +144,55 @@ def test_special_values_through_the_tables():
         st = hqmq.read_status(status)
         assert (st["n_outliers"], st["n_saturated"], st["n_nonfinite"]) == \
             (tally["n_outliers"], tally["n_saturated"], tally["n_nonfinite"])
+
+
+@pytest.mark.parametrize("Sk,Sv,capk,capv,tk,tv", [
+    (8, 32, 0, 64, True, True), (32, 8, 30, 0, True, True), (1, 48, 64, 7, True, True), (48, 11, 200, 200, True, False),
+    (3, 9, 0, 40, False, False)])
+@pytest.mark.parametrize("new", [[1, 0, 2], [70, 30, 0]])
+def test_k_and_v_of_different_kinds(Sk, Sv, capk, capv, tk, tv, new):
+    """Codebook sizes, flags, tables and pool sizes of their own; a page id that only K has."""
+    rng = np.random.default_rng(Sk + Sv)
+    old = [3, 5, 16]
+    table, n = layout(rng, [a + b for a, b in zip(old, new)], 32)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    last = table[0, (old[0] + new[0] - 1) // 32]
+    is_last, is_top = table == last, table == n - 1
+    table[is_top] = last
+    table[is_last] = n - 1                                            # K's last page, which V lacks
+    status, args, pools, xs = hqmq.new_status(), [], [], []
+    for S, cap, tab, pages in ((Sk, capk, tk, n), (Sv, capv, tv, n - 1)):
+        pool = P.empty_pool(rng, pages, 3, 32, S, cap)
+        if cap:
+            pool["flags"] &= np.uint32(0x01000010)
+        x, xf = tokens(rng, int(cu[-1]), 3, torch.float32)
+        args.append((*P.upload(pool, P.search_tables(pool["cb"]) if tab else None), x.cuda()))
+        pools.append(pool)
+        xs.append(xf)
+    (kp, kt, xk), (vp, vt, xv) = args
+    hqmq.hqmq_paged_write(xk, xv, kp, vp, *cuda_ints(table, cu, old), status=status)
+    bad = [P.write(pool, xf, table, cu, old)["bad"] for pool, xf in zip(pools, xs)]
+    assert bad[0] == 0 < bad[1]
+    P.assert_pools_equal(kt, pools[0])
+    P.assert_pools_equal(vt, pools[1])
+    assert hqmq.read_status(status)["flags"] & hqmq.FLAG_BAD_PAGE
+
+
+def test_as_many_heads_as_there_may_be():
+    rng = np.random.default_rng(43)
+    table, n = layout(rng, [20, 3], 16)
+    pool = P.empty_pool(rng, n, 1024, 16, 5, 9)
+    pool["flags"] &= np.uint32(0x00100001)
+    x, xf = tokens(rng, 5, 1024, torch.bfloat16)
+    kp, t = P.upload(pool)
+    hqmq.hqmq_paged_write(x.cuda(), None, kp, None, *cuda_ints(table, [0, 3, 5], [17, 1]))
+    P.write(pool, xf, table, [0, 3, 5], [17, 1])
+    P.assert_pools_equal(t, pool)
+    pool["words"] = F.pack_all(F.unpack_all(pool["words"], pool["words"].shape[3]) % (24 * 5), pool["words"].shape[3])
+    kp, _ = P.upload(pool)
+    y = torch.full((2, 1024, 20, 128), 7.0, device="cuda")
+    hqmq.hqmq_paged_read(kp, *cuda_ints(table, [20, 3]), y)
+    vals = F.values(pool)
+    for b, m in enumerate([20, 3]):
+        np.testing.assert_array_equal(y[b, :, :m].cpu().numpy(), F.dense(vals, table[b], m))
+        assert bool((y[b, :, m:] == 7).all())

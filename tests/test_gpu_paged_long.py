@@ -151,3 +151,14 @@ def test_rows_whose_scores_are_all_minus_infinity_count_as_empty():
         same[1, 0] = same[2, 3] = False
         assert torch.equal(o0[same], o1[same]) and torch.equal(lse0[same], lse1[same])
         x.q = base
+
+
+@pytest.mark.parametrize("out", [F32, BF])
+@pytest.mark.parametrize("B,Hk,G,lens,prefix", [
+    (1501, 1, 1, [0, 1, 0, 70, 2] * 300 + [0], 65), (700, 1, 1, [0] * 698 + [1, 0], 0), (2, 257, 2, [3, 130], 20),
+    (1, 1024, 16, [5], 0)])
+def test_many_sequences_and_many_heads(B, Hk, G, lens, prefix, out):
+    """Lists of segments that are mostly empty, and shares of many heads."""
+    x = F.Batch(10, B, Hk, G, 16, 3, 20, lens, prefix)
+    o, lse = x.call(out)
+    x.check(o, lse, WEIGHT[out])
