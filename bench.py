@@ -380,16 +380,28 @@ TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "traffic_encode_med3_call_llama
 TRAFFIC_SHAPE = ((1, 8, 131072, 128), 32)
 
 
-def kernel_sources_sha256():
-    """SHA-256 over the CUDA sources of the library (file name and contents,
-    in name order)."""
-    import glob
+# the kernels of that call and of hqmq_decode: k_sample_window and k_finalize, k_encode_spec, k_list_fix, k_decode
+TRAFFIC_SOURCES = ("med3_window.cu", "encode_spec.cu", "search.cu", "decode.cu")
+
+
+def kernel_sources_sha256(csrc=os.path.join(ROOT, "kv_cache_quantization_hqmq_b200", "csrc")):
+    """SHA-256 over the CUDA sources that the captured kernels are built from
+    (TRAFFIC_SOURCES and the headers beside them that they include; file name
+    and contents, in name order)."""
     import hashlib
+    import re
+    names, todo = set(), list(TRAFFIC_SOURCES)
+    while todo:
+        name = todo.pop()
+        if name in names:
+            continue
+        names.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            todo += [i for i in re.findall(r'^#include "([^"/]+)"', f.read(), re.M)]
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "kv_cache_quantization_hqmq_b200", "csrc")
-    for f in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
-        h.update(os.path.basename(f).encode())
-        with open(f, "rb") as fh:
+    for name in sorted(names):
+        h.update(name.encode())
+        with open(os.path.join(csrc, name), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()
 
